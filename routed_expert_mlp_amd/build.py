@@ -9,6 +9,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "moe_mlp.hip")
+ATTN_SRC = os.path.join(HERE, "csrc", "moe_attn.hip")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmoe_mlp.so")
 
@@ -28,19 +29,33 @@ def hipcc():
 
 
 def build(verbose=False):
+    """Compile both sources side by side and link them into LIB."""
     os.makedirs(LIB_DIR, exist_ok=True)
+    base = [hipcc()] + HIPCC_FLAGS
+    objs = [os.path.join(LIB_DIR, os.path.basename(src)[:-4] + ".o") for src in (SRC, ATTN_SRC)]
+    jobs = []
+    for src, obj in zip((SRC, ATTN_SRC), objs):
+        cmd = [f for f in base if f != "-shared"] + ["-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        jobs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), SRC, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    err = "\n".join(l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
-    if err.strip() and verbose:
-        print(err, file=sys.stderr)
+    outputs = [job.communicate()[0] for job in jobs]
+    for job, output in zip(jobs, outputs):
+        _check(output, job.returncode, verbose)
+    cmd = [base[0], "--offload-arch=gfx950", "-fPIC", "-shared"] + objs + ["-o", tmp]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    _check(r.stdout, r.returncode, verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def _check(output, status, verbose):
+    err = "\n".join(l for l in output.splitlines() if "packed-fp32-ops" not in l)
+    if status != 0:
+        raise RuntimeError(f"hipcc failed ({status}):\n{err}")
+    if err.strip() and verbose:
+        print(err, file=sys.stderr)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,206 @@
+// C ABI of the attention operators (declarations and contract in
+// include/moe_attn.h).  Host code: argument validation before anything is
+// enqueued, and the launches.  Nothing here allocates, synchronises or keeps
+// state.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_attn.h"
+#include "attn.hpp"
+#include "attn_prepare.hpp"
+#include "attn_simple.hpp"
+
+namespace {
+
+using namespace moe;
+
+constexpr int64_t kInt32End = int64_t(1) << 31;
+constexpr int64_t kMaxTokens = int64_t(1) << 26;   // rows of one call
+
+bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int page_shift_of(int32_t page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+int validate_cfg(const moe_attn_config* c) {
+  if (!c) return MOE_MLP_ERR_NULL_ARG;
+  if (c->n_heads < 1 || c->n_heads > MOE_ATTN_MAX_HEADS || c->n_kv_heads < 1 || c->n_heads % c->n_kv_heads != 0)
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_MLP_ERR_BAD_SHAPE;
+  if (page_shift_of(c->page_size) < 0) return MOE_MLP_ERR_BAD_SHAPE;
+  if (c->rotary_dim < 0 || c->rotary_dim > c->head_dim || c->rotary_dim % 16 != 0) return MOE_MLP_ERR_BAD_SHAPE;
+  if (c->rope_style != MOE_ATTN_ROPE_HALF && c->rope_style != MOE_ATTN_ROPE_INTERLEAVED)
+    return MOE_MLP_ERR_BAD_VALUE;
+  if (c->window < 0 || c->n_sinks < 0) return MOE_MLP_ERR_BAD_VALUE;
+  if (!std::isfinite(c->norm_eps) || c->norm_eps < 0.0f) return MOE_MLP_ERR_BAD_VALUE;
+  if (!std::isfinite(c->scale) || !(c->scale > 0.0f)) return MOE_MLP_ERR_BAD_VALUE;
+  return MOE_MLP_OK;
+}
+
+int validate_cache(const moe_attn_config* c, const moe_attn_cache* cache) {
+  if (!cache || !cache->k || !cache->v) return MOE_MLP_ERR_NULL_ARG;
+  if (cache->n_pages < 1 || cache->n_pages >= kInt32End / c->page_size) return MOE_MLP_ERR_BAD_SHAPE;
+  if (!aligned(cache->k) || !aligned(cache->v)) return MOE_MLP_ERR_MISALIGNED;
+  return MOE_MLP_OK;
+}
+
+// hipLaunchKernel says whether this launch failed; an error that an earlier
+// call of the process left behind is not taken for it.
+template <typename A>
+int launch(void (*kernel)(A), dim3 grid, dim3 block, hipStream_t s, A args) {
+  void* p[] = {&args};
+  if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, p, 0, s) == hipSuccess)
+    return MOE_MLP_OK;
+  (void)hipGetLastError();
+  return MOE_MLP_ERR_HIP;
+}
+
+// Calls f(std::integral_constant<int, head_dim>).
+template <typename F>
+int with_dim(int head_dim, F&& f) {
+  switch (head_dim) {
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    default: return f(std::integral_constant<int, 256>{});
+  }
+}
+
+// Sizes that both forms of attention check: B sequences, at most max_q new
+// tokens and max_len tokens of each.
+int validate_sizes(const moe_attn_config* c, int64_t B, int64_t max_q, int64_t max_len, int prefill) {
+  const int st = validate_cfg(c);
+  if (st) return st;
+  if (B < 0 || max_q < 0 || max_len < 0 || B >= kInt32End || max_q >= kInt32End || max_len >= kInt32End / 2)
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (!prefill && (max_q < 1 || max_q > MOE_ATTN_DECODE_MAX_Q)) return MOE_MLP_ERR_BAD_SHAPE;
+  if (B && max_q * c->n_heads >= kMaxTokens / B) return MOE_MLP_ERR_BAD_SHAPE;
+  return MOE_MLP_OK;
+}
+
+int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t T, const int32_t* cu_q,
+              int64_t B, int64_t max_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
+              int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream, int prefill) {
+  size_t need = 0;
+  int st = moe_attn_workspace_size(c, B, max_q, max_len, prefill, &need);
+  if (st) return st;
+  if (max_pages < 0 || max_pages >= kInt32End || max_len > max_pages * c->page_size) return MOE_MLP_ERR_BAD_SHAPE;
+  if (!prefill) T = B * max_q;
+  if (T < 0 || T >= kMaxTokens) return MOE_MLP_ERR_BAD_SHAPE;
+  if (B == 0 || T == 0 || max_q == 0) return MOE_MLP_OK;
+  st = validate_cache(c, cache);
+  if (st) return st;
+  if (!q || !out || !seq_lens || (prefill && !cu_q) || (max_len > 0 && !page_table)) return MOE_MLP_ERR_NULL_ARG;
+  if (need && !workspace) return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(q) || !aligned(out) || !aligned(workspace) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
+      !aligned(cu_q, 4))
+    return MOE_MLP_ERR_MISALIGNED;
+  if (ws_bytes < need) return MOE_MLP_ERR_WORKSPACE_TOO_SMALL;
+  AttnArgs a{};
+  a.q = q;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.out = out;
+  a.seq_lens = seq_lens;
+  a.page_table = page_table;
+  a.cu_q = prefill ? cu_q : nullptr;
+  a.ws = static_cast<float*>(workspace);
+  a.T = T;
+  a.max_pages = max_pages;
+  a.n_pages = static_cast<int32_t>(cache->n_pages);
+  a.B = static_cast<int32_t>(B);
+  a.n_q = static_cast<int32_t>(max_q);
+  a.max_len = static_cast<int32_t>(max_len);
+  a.heads = c->n_heads;
+  a.kv_heads = c->n_kv_heads;
+  a.group = c->n_heads / c->n_kv_heads;
+  a.page_shift = page_shift_of(c->page_size);
+  a.window = c->window;
+  a.sinks = c->n_sinks;
+  a.scale_log2 = c->scale * 1.44269504088896340736f;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return with_dim(c->head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    return launch(k_attn_row<D>, dim3(static_cast<unsigned>(B * max_q * c->n_heads)), dim3(64), s, a);
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* qkv,
+                     int64_t qkv_stride, int64_t T, const float* q_norm_w, const float* k_norm_w,
+                     const float* cos_sin, int64_t n_positions, const int32_t* positions, const int64_t* slots,
+                     uint16_t* q_out, void* stream) {
+  int st = validate_cfg(cfg);
+  if (st) return st;
+  const int64_t rows = cfg->n_heads + 2 * int64_t(cfg->n_kv_heads);
+  if (T < 0 || T >= kMaxTokens || qkv_stride < rows * cfg->head_dim || qkv_stride % 8 != 0 ||
+      qkv_stride >= kInt32End)
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (cfg->rotary_dim && n_positions < 1) return MOE_MLP_ERR_BAD_SHAPE;
+  if (T == 0) return MOE_MLP_OK;
+  st = validate_cache(cfg, cache);
+  if (st) return st;
+  if (!qkv || !slots || !q_out || (cfg->rotary_dim && (!cos_sin || !positions))) return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(qkv) || !aligned(q_out) || !aligned(q_norm_w) || !aligned(k_norm_w) || !aligned(cos_sin) ||
+      !aligned(positions, 4) || !aligned(slots, 8))
+    return MOE_MLP_ERR_MISALIGNED;
+  PrepArgs a{};
+  a.qkv = qkv;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.q_out = q_out;
+  a.qw = q_norm_w;
+  a.kw = k_norm_w;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.stride = qkv_stride;
+  a.T = T;
+  a.n_positions = n_positions;
+  a.n_slots = cache->n_pages * cfg->page_size;
+  a.heads = cfg->n_heads;
+  a.kv_heads = cfg->n_kv_heads;
+  a.page_shift = page_shift_of(cfg->page_size);
+  a.rotary = cfg->rotary_dim;
+  a.interleaved = cfg->rope_style == MOE_ATTN_ROPE_INTERLEAVED;
+  a.eps = cfg->norm_eps;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return with_dim(cfg->head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    return launch(k_attn_prepare<D>, dim3(static_cast<unsigned>(cdiv(T, 2048 / D)), static_cast<unsigned>(rows)),
+                  dim3(256), s, a);
+  });
+}
+
+int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t max_q, int64_t max_len, int prefill,
+                            size_t* bytes) {
+  const int st = validate_sizes(cfg, B, max_q, max_len, prefill);
+  if (st) return st;
+  if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = 0;
+  return MOE_MLP_OK;
+}
+
+int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,
+                    int64_t n_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
+                    int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+  return attention(cfg, cache, q, 0, nullptr, B, n_q, seq_lens, page_table, max_pages, max_len, out, workspace,
+                   ws_bytes, stream, 0);
+}
+
+int moe_attn_prefill(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t T,
+                     const int32_t* cu_q, int64_t B, int64_t max_q, const int32_t* seq_lens,
+                     const int32_t* page_table, int64_t max_pages, int64_t max_len, uint16_t* out, void* workspace,
+                     size_t ws_bytes, void* stream) {
+  return attention(cfg, cache, q, T, cu_q, B, max_q, seq_lens, page_table, max_pages, max_len, out, workspace,
+                   ws_bytes, stream, 1);
+}
+
+}  // extern "C"

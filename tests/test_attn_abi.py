@@ -1,0 +1,163 @@
+"""C ABI of the attention operators without a GPU: the library exports what
+include/moe_attn.h declares and refuses bad arguments before anything is
+enqueued (so fake device addresses are safe)."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+
+from routed_expert_mlp_amd import attention as A
+from routed_expert_mlp_amd import capi
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x7F0000000000
+BIG = 1 << 40
+
+
+def cfg(**kw):
+    base = dict(n_heads=8, n_kv_heads=2, head_dim=128, page_size=16, rotary_dim=64, rope_style=0, window=0, n_sinks=0,
+                norm_eps=1e-6, scale=0.1)
+    base.update(kw)
+    return A.moe_attn_config(**base)
+
+
+def cache(**kw):
+    base = dict(k=FAKE, v=FAKE + 0x100000, n_pages=8)
+    base.update(kw)
+    return A.moe_attn_cache(**base)
+
+
+def size(c, B=2, max_q=1, max_len=64, prefill=0):
+    n = ctypes.c_size_t(0)
+    st = A._lib().moe_attn_workspace_size(ctypes.byref(c) if c is not None else None, B, max_q, max_len, prefill,
+                                          ctypes.byref(n))
+    return st, n.value
+
+
+def decode(c, cc, B=2, n_q=1, max_pages=4, max_len=64, q=FAKE, lens=FAKE, table=FAKE, out=FAKE, ws=FAKE, wsb=BIG):
+    return A._lib().moe_attn_decode(ctypes.byref(c) if c is not None else None,
+                                    ctypes.byref(cc) if cc is not None else None, q, B, n_q, lens, table, max_pages,
+                                    max_len, out, ws, wsb, None)
+
+
+def prefill(c, cc, T=4, B=2, max_q=4, max_pages=4, max_len=64, q=FAKE, cu=FAKE, lens=FAKE, table=FAKE, out=FAKE,
+            ws=FAKE, wsb=BIG):
+    return A._lib().moe_attn_prefill(ctypes.byref(c) if c is not None else None,
+                                     ctypes.byref(cc) if cc is not None else None, q, T, cu, B, max_q, lens, table,
+                                     max_pages, max_len, out, ws, wsb, None)
+
+
+def prepare(c, cc, T=2, stride=12 * 128, qkv=FAKE, qw=FAKE, kw=FAKE, cs=FAKE, P=10, pos=FAKE, slots=FAKE, q=FAKE):
+    return A._lib().moe_attn_prepare(ctypes.byref(c) if c is not None else None,
+                                     ctypes.byref(cc) if cc is not None else None, qkv, stride, T, qw, kw, cs, P, pos,
+                                     slots, q, None)
+
+
+ALL = [decode, prefill, prepare]
+
+
+def test_library_exports_every_declared_function():
+    text = open(os.path.join(ROOT, "include", "moe_attn.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"^\s*(?:const\s+)?\w+\s*\**\s*(moe_\w+)\s*\(", text, flags=re.M))
+    assert names == set(A.EXPORTED)
+    for n in names:
+        assert getattr(A._lib(), n) is not None
+
+
+@pytest.mark.parametrize("call", ALL)
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_heads=0), capi.ERR_BAD_SHAPE), (dict(n_heads=7), capi.ERR_BAD_SHAPE),
+    (dict(n_heads=2048), capi.ERR_BAD_SHAPE), (dict(n_kv_heads=0), capi.ERR_BAD_SHAPE),
+    (dict(n_kv_heads=-2), capi.ERR_BAD_SHAPE), (dict(n_kv_heads=16), capi.ERR_BAD_SHAPE),
+    (dict(head_dim=96), capi.ERR_BAD_SHAPE), (dict(head_dim=0), capi.ERR_BAD_SHAPE),
+    (dict(page_size=8), capi.ERR_BAD_SHAPE), (dict(page_size=48), capi.ERR_BAD_SHAPE),
+    (dict(page_size=512), capi.ERR_BAD_SHAPE), (dict(rotary_dim=-16), capi.ERR_BAD_SHAPE),
+    (dict(rotary_dim=8), capi.ERR_BAD_SHAPE), (dict(rotary_dim=144), capi.ERR_BAD_SHAPE),
+    (dict(rope_style=2), capi.ERR_BAD_VALUE), (dict(window=-1), capi.ERR_BAD_VALUE),
+    (dict(n_sinks=-1), capi.ERR_BAD_VALUE), (dict(norm_eps=-1.0), capi.ERR_BAD_VALUE),
+    (dict(norm_eps=math.nan), capi.ERR_BAD_VALUE), (dict(scale=0.0), capi.ERR_BAD_VALUE),
+    (dict(scale=-1.0), capi.ERR_BAD_VALUE), (dict(scale=math.inf), capi.ERR_BAD_VALUE),
+    (dict(scale=math.nan), capi.ERR_BAD_VALUE),
+])
+def test_config_validation(call, kw, code):
+    assert call(cfg(**kw), cache()) == code
+    assert size(cfg(**kw))[0] == code
+
+
+@pytest.mark.parametrize("call", ALL)
+def test_null_and_cache(call):
+    assert call(None, cache()) == capi.ERR_NULL_ARG
+    assert call(cfg(), None) == capi.ERR_NULL_ARG
+    assert call(cfg(), cache(k=None)) == capi.ERR_NULL_ARG
+    assert call(cfg(), cache(v=None)) == capi.ERR_NULL_ARG
+    assert call(cfg(), cache(n_pages=0)) == capi.ERR_BAD_SHAPE
+    assert call(cfg(), cache(n_pages=-1)) == capi.ERR_BAD_SHAPE
+    assert call(cfg(), cache(n_pages=1 << 27)) == capi.ERR_BAD_SHAPE
+    assert call(cfg(), cache(k=FAKE + 8)) == capi.ERR_MISALIGNED
+    assert call(cfg(), cache(v=FAKE + 2)) == capi.ERR_MISALIGNED
+
+
+@pytest.mark.parametrize("call,names", [(decode, ("q", "lens", "table", "out")),
+                                        (prefill, ("q", "cu", "lens", "table", "out")),
+                                        (prepare, ("qkv", "cs", "pos", "slots", "q"))])
+def test_null_arguments(call, names):
+    for n in names:
+        assert call(cfg(), cache(), **{n: None}) == capi.ERR_NULL_ARG, n
+
+
+@pytest.mark.parametrize("call,off", [(decode, dict(q=8, lens=2, table=1, out=4, ws=8)),
+                                      (prefill, dict(q=8, cu=2, lens=2, table=3, out=4, ws=4)),
+                                      (prepare, dict(qkv=8, qw=4, kw=8, cs=4, pos=2, slots=4, q=2))])
+def test_misaligned_arguments(call, off):
+    for n, d in off.items():
+        assert call(cfg(), cache(), **{n: FAKE + d}) == capi.ERR_MISALIGNED, n
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(n_q=0), dict(n_q=9), dict(n_q=-1), dict(max_len=-1),
+                                dict(max_len=65), dict(max_pages=-1), dict(max_pages=3), dict(B=1 << 60),
+                                dict(B=1 << 62, n_q=8), dict(max_len=1 << 62, max_pages=1 << 62),
+                                dict(max_len=1 << 30, max_pages=1 << 30), dict(B=1 << 24)])
+def test_decode_sizes(kw):
+    assert decode(cfg(), cache(), **kw) == capi.ERR_BAD_SHAPE
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(T=-1), dict(max_q=-1), dict(max_len=65), dict(max_pages=3),
+                                dict(T=1 << 26), dict(T=1 << 62), dict(max_q=1 << 62), dict(B=1 << 62),
+                                dict(B=1 << 20, max_q=1 << 10)])
+def test_prefill_sizes(kw):
+    assert prefill(cfg(), cache(), **kw) == capi.ERR_BAD_SHAPE
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(T=1 << 40), dict(stride=12 * 128 - 8), dict(stride=12 * 128 + 4),
+                                dict(stride=1 << 40), dict(stride=-12 * 128), dict(P=0), dict(P=-5)])
+def test_prepare_sizes(kw):
+    assert prepare(cfg(), cache(), **kw) == capi.ERR_BAD_SHAPE
+
+
+def test_nothing_to_do_is_ok():
+    assert decode(cfg(), None, B=0, q=None, lens=None, table=None, out=None, ws=None, wsb=0) == capi.OK
+    assert prefill(cfg(), None, T=0, q=None, cu=None, out=None, ws=None, wsb=0) == capi.OK
+    assert prefill(cfg(), None, B=0, q=None, cu=None, lens=None, table=None, out=None, ws=None, wsb=0) == capi.OK
+    assert prefill(cfg(), None, max_q=0, q=None, cu=None, out=None, ws=None, wsb=0) == capi.OK
+    assert prepare(cfg(), None, T=0, qkv=None, cs=None, pos=None, slots=None, q=None) == capi.OK
+
+
+def test_workspace_size_and_refusal():
+    for pf, call in ((0, decode), (1, prefill)):
+        assert size(cfg(), prefill=pf, max_len=1 << 62)[0] == capi.ERR_BAD_SHAPE
+        st, need = size(cfg(), B=2, max_q=4, max_len=64, prefill=pf)
+        assert st == capi.OK
+    # long caches of few rows are split and joined: that needs room
+    long = dict(B=1, max_len=131072)
+    st, need = size(cfg(), max_q=1, prefill=0, **long)
+    assert st == capi.OK
+    if need:
+        assert decode(cfg(), cache(), max_pages=8192, wsb=need - 1, **long) == capi.ERR_WORKSPACE_TOO_SMALL
+        assert decode(cfg(), cache(), max_pages=8192, ws=None, wsb=0, **long) == capi.ERR_NULL_ARG
+    n = ctypes.c_size_t(0)
+    c = cfg()
+    assert A._lib().moe_attn_workspace_size(ctypes.byref(c), 1, 1, 16, 0, None) == capi.ERR_NULL_ARG
+    assert n.value == 0
