@@ -10,6 +10,8 @@
 
 namespace moe {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 struct AttnArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -26,6 +28,7 @@ struct AttnArgs {
   int32_t heads, kv_heads, group;
   int32_t page_shift;
   int32_t window, sinks;      // window 0: none
+  int32_t splits, tiles_per_split;   // decode: parts of the visible tiles
   float scale_log2;           // scale * log2(e): the softmax runs on exp2
 };
 
@@ -58,5 +61,57 @@ __device__ __forceinline__ int attn_window_lo(const AttnArgs& a, int p) {
 __device__ __forceinline__ bool attn_visible(int key, int p, int lo, int sinks) {
   return key <= p && (key >= lo || key < sinks);
 }
+
+// The tiles of TS keys that hold a key visible to any of the positions
+// first .. last (consecutive, so their windows join up): tiles 0 .. na-1 hold
+// the sinks, tiles b0 .. the window up to key `last`; n in all.
+struct AttnTiles {
+  int na, b0, n;
+  int lo, hi, sinks;        // visible to some position: key < hi and (key >= lo or key < sinks)
+  __device__ __forceinline__ int tile(int v) const { return v < na ? v : v - na + b0; }
+};
+
+template <int TS>
+__device__ __forceinline__ AttnTiles attn_tiles(const AttnArgs& a, int first, int last) {
+  AttnTiles t;
+  t.hi = max(last + 1, 0);
+  t.lo = attn_window_lo(a, first);
+  t.sinks = a.window ? a.sinks : 0;
+  t.b0 = t.lo / TS;
+  t.na = (min(t.sinks, t.hi) + TS - 1) / TS;
+  if (t.na >= t.b0) t.na = t.b0 = 0;
+  t.n = t.na + (t.hi + TS - 1) / TS - t.b0;
+  if (t.hi == 0) t.n = 0;
+  return t;
+}
+
+// 32x32x16 MFMA, C = A B: lane l holds column l % 32 and rows
+// 8 (e / 4) + 4 (l / 32) + e % 4 (e = 0..15) of C, and 8 reduction elements
+// 8 (l / 32) .. +7 of row (column) l % 32 of A (B).
+//
+// Scores are computed transposed, keys x queries, so that a lane's 16 values
+// belong to one query: its softmax needs one exchange between lanes l and
+// l + 32, and the values go back in as the B operand of V^T P^T without any
+// other exchange, provided the keys sit in the tile's rows in the right order:
+// with key swap23(r) in row r (bits 2 and 3 swapped) value e of lane l is key
+// 16 (e / 8) + 8 (l / 32) + e % 8, which is element e % 8 of that operand.
+__device__ __forceinline__ int swap23(int r) { return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1); }
+__device__ __forceinline__ int score_key(int e, int half) { return 16 * (e >> 3) + 8 * half + (e & 7); }
+
+// v of lane l and of lane l ^ 32, larger of the two.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Below every score, and finite: the running maximum of a row that has seen nothing.
+constexpr float ATTN_NO_MAX = -1e30f;
 
 }  // namespace moe

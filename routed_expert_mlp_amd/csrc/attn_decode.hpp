@@ -1,0 +1,333 @@
+// Attention of a few new tokens of each sequence over the paged cache, split
+// over the cache's length and joined.
+//
+//   out = sum_k p_k v_k / sum_k p_k,  p_k = exp2(c q.k - m),  c = scale log2(e)
+//
+// with the running maximum m per query, in one pass over the keys.
+//
+// What bounds it: every key and value row is read once for all query heads of
+// its group and all new tokens (4 D bytes for 4 D flops per column), so the
+// stream from HBM is the floor; the matrix instructions, which carry the
+// group's heads as columns of one operand, take a few percent of that time
+// even with most columns empty.  So:
+//   * K and V go from HBM straight into the operand registers of the matrix
+//     instructions, 16 bytes a lane and whole lines an instruction, with no
+//     LDS and no transposition: that is what the cache's layout is for;
+//   * one block is 8 wavefronts (4 at 256 dims) that take tiles of 32 keys in
+//     turn, each with its next tile's keys and values in flight while it
+//     works on the present one; they join their parts in LDS;
+//   * the visible tiles of a sequence are cut into parts of tiles_per_split,
+//     a block each; a sequence with one part is done by then, the others'
+//     parts (unnormalised sums, maximum and sum, in fp32) are joined by
+//     k_attn_join.
+#pragma once
+
+#include "attn.hpp"
+
+namespace moe {
+
+constexpr int ATTN_MAX_TPS = 64;      // most 32-key tiles of a part
+
+// Wavefronts of a block: 8 while a wavefront's sums and operands fit 256
+// registers, else 4 with up to 512.
+template <int D, int CT>
+struct DecodeShape {
+  static constexpr int NW = D * CT >= 256 ? 4 : 8;
+};
+
+// Column col of a sequence and key/value head: new token col / group, head col % group.
+__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnSeq& s, int kvh, int col) {
+  const int t = col / a.group;
+  return (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
+}
+
+template <int D, int CT>
+__global__ __launch_bounds__((DecodeShape<D, CT>::NW) * 64, 1) void k_attn_decode(AttnArgs a) {
+  constexpr int NW = DecodeShape<D, CT>::NW, KS = D / 16, DT = D / 32, COLS = 32 * CT, LD = D + 4;
+  const int cols = a.n_q * a.group;
+  const int col_blocks = (cols + COLS - 1) / COLS;
+  int bi = blockIdx.x;
+  const int split = bi % a.splits;
+  bi /= a.splits;
+  const int cb = bi % col_blocks;
+  bi /= col_blocks;
+  const int kvh = bi % a.kv_heads, b = bi / a.kv_heads;
+  const AttnSeq s = attn_seq(a, b);
+  const int first = s.len - s.n;
+  const AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
+  const int v0 = split * a.tiles_per_split, v1 = min(v0 + a.tiles_per_split, tl.n);
+  if (v0 >= v1 && split > 0) return;
+  const bool whole = tl.n <= a.tiles_per_split;
+
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r = lane & 31, half = lane >> 5;
+  __shared__ int ids[2 * ATTN_MAX_TPS];
+  __shared__ float lm[NW][COLS], ll[NW][COLS];
+  __shared__ float lo_[NW / 2][COLS * LD];
+
+  // page of each 16 keys of this part
+  for (int i = tid; i < 2 * (v1 - v0); i += NW * 64) {
+    const int key = min(32 * tl.tile(v0 + (i >> 1)) + 16 * (i & 1), s.len - 1);
+    ids[i] = min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
+  }
+
+  bf16x8 qf[CT][KS];
+  int pos[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int col = min(cb * COLS + 32 * ct + r, cols - 1);
+    pos[ct] = first + col / a.group;
+    const uint16_t* qp = a.q + attn_row(a, s, kvh, col) * D + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) qf[ct][ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
+  }
+  __syncthreads();
+
+  const int ps = 1 << a.page_shift;
+  const int64_t head_elems = static_cast<int64_t>(D) << a.page_shift;
+  auto load_k = [&](int v, uint4 (&kf)[KS]) {
+    const int key = 32 * tl.tile(v) + swap23(r);
+    const int64_t base = (static_cast<int64_t>(ids[2 * (v - v0) + (r >> 4)]) * a.kv_heads + kvh) * head_elems +
+                         ((half << a.page_shift) + (key & (ps - 1))) * 8;
+    const uint16_t* p = a.k + base;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const uint4*>(p + ((2 * ks * 8) << a.page_shift));
+  };
+  auto load_v = [&](int v, uint4 (&vf)[2][DT]) {
+    const int key0 = 32 * tl.tile(v);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int at = ((key0 + 16 * g) & (ps - 1)) + 8 * half;
+      const uint16_t* p = a.v + (static_cast<int64_t>(ids[2 * (v - v0) + g]) * a.kv_heads + kvh) * head_elems +
+                          at * D + r * 8;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) vf[g][dt] = *reinterpret_cast<const uint4*>(p + 32 * 8 * dt);
+    }
+  };
+
+  f32x16 acc[CT][DT];
+  float m[CT], l[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    m[ct] = ATTN_NO_MAX;
+    l[ct] = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[ct][dt][e] = 0.0f;
+  }
+  uint4 kf[KS], vf[2][DT];
+  int v = v0 + w;
+  if (v < v1) {
+    load_k(v, kf);
+    load_v(v, vf);
+  }
+  for (; v < v1; v += NW) {
+    f32x16 sc[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[ct][e] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        sc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[ks]), qf[ct][ks], sc[ct], 0, 0,
+                                                         0);
+    const int vn = v + NW;
+    if (vn < v1) load_k(vn, kf);
+    const int key0 = 32 * tl.tile(v);
+    // a tile that some column sees only in part: scores of invisible keys go to
+    // -inf, and the values of keys that nobody sees, whatever the slots hold, to 0
+    if (key0 + 31 > first || (a.window && key0 < max(0, s.len - a.window) && key0 + 31 >= tl.sinks)) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const int wlo = attn_window_lo(a, pos[ct]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!attn_visible(key0 + score_key(e, half), pos[ct], wlo, tl.sinks)) sc[ct][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t mk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int ka = key0 + 16 * g + 8 * half + 2 * j;
+          const bool sa = ka < tl.hi && (ka >= tl.lo || ka < tl.sinks);
+          const bool sb = ka + 1 < tl.hi && (ka + 1 >= tl.lo || ka + 1 < tl.sinks);
+          mk[j] = (sa ? 0xFFFFu : 0u) | (sb ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          vf[g][dt].x &= mk[0];
+          vf[g][dt].y &= mk[1];
+          vf[g][dt].z &= mk[2];
+          vf[g][dt].w &= mk[3];
+        }
+      }
+    }
+    uint4 pf[CT][2];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float mx = sc[ct][0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[ct][e]);
+      const float mn = fmaxf(m[ct], max_halves(mx) * a.scale_log2);
+      if (__any(mn > m[ct])) {
+        const float f = exp2_fast(m[ct] - mn);
+        m[ct] = mn;
+        l[ct] *= f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[ct][dt][e] *= f;
+      }
+      uint32_t pk[8];
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float p0 = exp2_fast(fmaf(sc[ct][e], a.scale_log2, -m[ct]));
+        const float p1 = exp2_fast(fmaf(sc[ct][e + 1], a.scale_log2, -m[ct]));
+        l[ct] += p0 + p1;
+        pk[e >> 1] = pack_bf16x2(p0, p1);
+      }
+      pf[ct][0] = {pk[0], pk[1], pk[2], pk[3]};
+      pf[ct][1] = {pk[4], pk[5], pk[6], pk[7]};
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          acc[ct][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g][dt]),
+                                                                __builtin_bit_cast(bf16x8, pf[ct][g]), acc[ct][dt], 0,
+                                                                0, 0);
+    if (vn < v1) load_v(vn, vf);
+  }
+
+  // join the wavefronts: common maximum, then the sums in a tree
+  const int live = min(cols - cb * COLS, COLS);
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const float lt = sum_halves(l[ct]);
+    if (half == 0) {
+      lm[w][32 * ct + r] = m[ct];
+      ll[w][32 * ct + r] = lt;
+    }
+  }
+  __syncthreads();
+  float M[CT], L[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    M[ct] = lm[0][32 * ct + r];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) M[ct] = fmaxf(M[ct], lm[i][32 * ct + r]);
+    L[ct] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) L[ct] += ll[i][32 * ct + r] * exp2_fast(lm[i][32 * ct + r] - M[ct]);
+    const float f = exp2_fast(m[ct] - M[ct]);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[ct][dt][e] *= f;
+  }
+#pragma unroll
+  for (int step = NW / 2; step; step >>= 1) {
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (32 * ct + r < live && w >= step && w < 2 * step) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(&lo_[w - step][(32 * ct + r) * LD + 32 * dt + 8 * i + 4 * half]) =
+                f32x4{acc[ct][dt][4 * i], acc[ct][dt][4 * i + 1], acc[ct][dt][4 * i + 2], acc[ct][dt][4 * i + 3]};
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (32 * ct + r < live && w < step) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(&lo_[w][(32 * ct + r) * LD + 32 * dt + 8 * i + 4 * half]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[ct][dt][4 * i + j] += o[j];
+          }
+      }
+    }
+  }
+  if (w != 0) return;
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    if (32 * ct + r >= live) continue;
+    const int col = cb * COLS + 32 * ct + r;
+    if (whole) {
+      const float inv = L[ct] > 0.0f ? 1.0f / L[ct] : 0.0f;
+      uint16_t* o = a.out + attn_row(a, s, kvh, col) * D + 4 * half;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint2 p = {pack_bf16x2(acc[ct][dt][4 * i] * inv, acc[ct][dt][4 * i + 1] * inv),
+                           pack_bf16x2(acc[ct][dt][4 * i + 2] * inv, acc[ct][dt][4 * i + 3] * inv)};
+          *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
+        }
+    } else {
+      const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits + split;
+      const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
+      if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + item * 2) = float2{M[ct], L[ct]};
+      float* o = a.ws + item * D + 4 * half;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4*>(o + 32 * dt + 8 * i) =
+              f32x4{acc[ct][dt][4 * i], acc[ct][dt][4 * i + 1], acc[ct][dt][4 * i + 2], acc[ct][dt][4 * i + 3]};
+    }
+  }
+}
+
+// Joins the parts of one output row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// Four wavefronts take every fourth part, D / 64 dims a lane.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  constexpr int ND = D / 64;
+  const int cols = a.n_q * a.group;
+  const int col = blockIdx.x % cols, kvh = (blockIdx.x / cols) % a.kv_heads, b = blockIdx.x / cols / a.kv_heads;
+  const AttnSeq s = attn_seq(a, b);
+  const AttnTiles tl = attn_tiles<32>(a, s.len - s.n, s.len - 1);
+  if (tl.n <= a.tiles_per_split) return;
+  const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
+  const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits;
+  const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + items * D) + item;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float M = ATTN_NO_MAX;
+  for (int i = lane; i < parts; i += 64) M = fmaxf(M, ml[i].x);
+#pragma unroll
+  for (int x = 32; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
+  float o[ND] = {}, L = 0.0f;
+  for (int i = w; i < parts; i += 4) {
+    const float2 p = ml[i];
+    const float f = exp2_fast(p.x - M);
+    L += p.y * f;
+    const float* src = a.ws + (item + i) * D + lane * ND;
+#pragma unroll
+    for (int n = 0; n < ND; ++n) o[n] += src[n] * f;
+  }
+  __shared__ float lo_[4][D], ll[4];
+#pragma unroll
+  for (int n = 0; n < ND; ++n) lo_[w][lane * ND + n] = o[n];
+  if (lane == 0) ll[w] = L;
+  __syncthreads();
+  const float t = (ll[0] + ll[1]) + (ll[2] + ll[3]);
+  const float inv = t > 0.0f ? 1.0f / t : 0.0f;
+  uint16_t* out = a.out + attn_row(a, s, kvh, col) * D;
+  for (int d = threadIdx.x; d < D; d += 256)
+    out[d] = f32_to_bf16(((lo_[0][d] + lo_[1][d]) + (lo_[2][d] + lo_[3][d])) * inv);
+}
+
+}  // namespace moe

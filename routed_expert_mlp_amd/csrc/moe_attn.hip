@@ -9,6 +9,7 @@
 
 #include "../../include/moe_attn.h"
 #include "attn.hpp"
+#include "attn_decode.hpp"
 #include "attn_prepare.hpp"
 #include "attn_simple.hpp"
 
@@ -82,6 +83,41 @@ int validate_sizes(const moe_attn_config* c, int64_t B, int64_t max_q, int64_t m
   return MOE_MLP_OK;
 }
 
+// How a decode call is cut: columns (new tokens x query heads of a key/value
+// head) in blocks of 32 * ct, the visible tiles of 32 keys in parts.
+struct DecodePlan {
+  int ct, col_blocks, splits, tiles_per_split;
+  size_t ws_bytes;
+};
+
+DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len) {
+  DecodePlan p{};
+  const int64_t cols = n_q * (c->n_heads / c->n_kv_heads);
+  p.ct = cols > 32 && c->head_dim != 256 ? 2 : 1;
+  p.col_blocks = static_cast<int>(cdiv(cols, 32 * p.ct));
+  int64_t tiles = cdiv(max_len, 32);
+  if (c->window) {
+    const int64_t seen = cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32);
+    if (seen < tiles) tiles = seen;
+  }
+  const int64_t nw = c->head_dim * p.ct >= 256 ? 4 : 8;
+  // parts of nw tiles, twice as many, ... until one block per CU is left
+  int64_t tps = nw;
+  while (tps < ATTN_MAX_TPS && B * c->n_kv_heads * p.col_blocks * cdiv(tiles, tps) > 1024) tps *= 2;
+  p.tiles_per_split = static_cast<int>(tps);
+  p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  if (p.splits > 1) p.ws_bytes = size_t(B) * c->n_kv_heads * cols * p.splits * (c->head_dim + 2) * 4;
+  return p;
+}
+
+template <int D, int CT>
+int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
+  const int64_t blocks = int64_t(a.B) * a.kv_heads * p.col_blocks * p.splits;
+  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(blocks)), dim3(DecodeShape<D, CT>::NW * 64), s, a);
+  if (st || p.splits == 1) return st;
+  return launch(k_attn_join<D>, dim3(static_cast<unsigned>(int64_t(a.B) * a.n_q * a.heads)), dim3(256), s, a);
+}
+
 int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t T, const int32_t* cu_q,
               int64_t B, int64_t max_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
               int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream, int prefill) {
@@ -123,6 +159,17 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
   a.sinks = c->n_sinks;
   a.scale_log2 = c->scale * 1.44269504088896340736f;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!prefill) {
+    const DecodePlan p = decode_plan(c, B, max_q, max_len);
+    a.splits = p.splits;
+    a.tiles_per_split = p.tiles_per_split;
+    return with_dim(c->head_dim, [&](auto dc) {
+      constexpr int D = decltype(dc)::value;
+      if constexpr (D != 256)
+        if (p.ct == 2) return decode<D, 2>(a, p, s);
+      return decode<D, 1>(a, p, s);
+    });
+  }
   return with_dim(c->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
     return launch(k_attn_row<D>, dim3(static_cast<unsigned>(B * max_q * c->n_heads)), dim3(64), s, a);
@@ -184,7 +231,7 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t max_q
   const int st = validate_sizes(cfg, B, max_q, max_len, prefill);
   if (st) return st;
   if (!bytes) return MOE_MLP_ERR_NULL_ARG;
-  *bytes = 0;
+  *bytes = prefill ? 0 : decode_plan(cfg, B, max_q, max_len).ws_bytes;
   return MOE_MLP_OK;
 }
 
