@@ -58,10 +58,6 @@ __device__ __forceinline__ int attn_window_lo(const AttnArgs& a, int p) {
   return a.window ? max(0, p - a.window + 1) : 0;
 }
 
-__device__ __forceinline__ bool attn_visible(int key, int p, int lo, int sinks) {
-  return key <= p && (key >= lo || key < sinks);
-}
-
 // The tiles of TS keys that hold a key visible to any of the positions
 // first .. last (consecutive, so their windows join up): tiles 0 .. na-1 hold
 // the sinks, tiles b0 .. the window up to key `last`; n in all.
@@ -97,6 +93,31 @@ __device__ __forceinline__ AttnTiles attn_tiles(const AttnArgs& a, int first, in
 // 16 (e / 8) + 8 (l / 32) + e % 8, which is element e % 8 of that operand.
 __device__ __forceinline__ int swap23(int r) { return (r & ~12) | ((r & 4) << 1) | ((r & 8) >> 1); }
 __device__ __forceinline__ int score_key(int e, int half) { return 16 * (e >> 3) + 8 * half + (e & 7); }
+
+// Bits 0 .. n-1.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+}
+
+// Bit j: key key0 + j is visible to position p with window start lo:
+// key <= p and (key >= lo or key < sinks).
+__device__ __forceinline__ uint64_t visible_bits(int key0, int p, int lo, int sinks) {
+  return low_bits(p + 1 - key0) & (~low_bits(lo - key0) | low_bits(sinks - key0));
+}
+
+// x where bit `bit` of the mask is set, else -inf.
+__device__ __forceinline__ float keep_if(uint32_t mask, int bit, float x) {
+  const uint32_t t = static_cast<uint32_t>(static_cast<int32_t>(mask << (31 - bit)) >> 31);
+  return __uint_as_float((__float_as_uint(x) & t) | (0xFF800000u & ~t));
+}
+
+// The same mask for the 8 values of 8 keys (4 words of 2): bits 0..7.
+__device__ __forceinline__ uint4 value_mask(uint32_t bits) {
+  auto w = [&](int j) { return (bits >> j & 1 ? 0xFFFFu : 0u) | (bits >> (j + 1) & 1 ? 0xFFFF0000u : 0u); };
+  return uint4{w(0), w(2), w(4), w(6)};
+}
+
+__device__ __forceinline__ uint4 and4(uint4 a, uint4 b) { return uint4{a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w}; }
 
 // v of lane l and of lane l ^ 32, larger of the two.
 __device__ __forceinline__ float max_halves(float v) {

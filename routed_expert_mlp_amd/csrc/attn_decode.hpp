@@ -141,28 +141,17 @@ __global__ __launch_bounds__((DecodeShape<D, CT>::NW) * 64, 1) void k_attn_decod
     if (key0 + 31 > first || (a.window && key0 < max(0, s.len - a.window) && key0 + 31 >= tl.sinks)) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        const int wlo = attn_window_lo(a, pos[ct]);
+        const uint32_t see = static_cast<uint32_t>(
+            visible_bits(key0 + 8 * half, pos[ct], attn_window_lo(a, pos[ct]), tl.sinks));
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (!attn_visible(key0 + score_key(e, half), pos[ct], wlo, tl.sinks)) sc[ct][e] = -INFINITY;
+        for (int e = 0; e < 16; ++e) sc[ct][e] = keep_if(see, 16 * (e >> 3) + (e & 7), sc[ct][e]);
       }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        uint32_t mk[4];
+        const uint4 mk = value_mask(static_cast<uint32_t>(
+            visible_bits(key0 + 16 * g + 8 * half, tl.hi - 1, tl.lo, tl.sinks)));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ka = key0 + 16 * g + 8 * half + 2 * j;
-          const bool sa = ka < tl.hi && (ka >= tl.lo || ka < tl.sinks);
-          const bool sb = ka + 1 < tl.hi && (ka + 1 >= tl.lo || ka + 1 < tl.sinks);
-          mk[j] = (sa ? 0xFFFFu : 0u) | (sb ? 0xFFFF0000u : 0u);
-        }
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          vf[g][dt].x &= mk[0];
-          vf[g][dt].y &= mk[1];
-          vf[g][dt].z &= mk[2];
-          vf[g][dt].w &= mk[3];
-        }
+        for (int dt = 0; dt < DT; ++dt) vf[g][dt] = and4(vf[g][dt], mk);
       }
     }
     uint4 pf[CT][2];

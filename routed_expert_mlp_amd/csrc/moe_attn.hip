@@ -10,8 +10,8 @@
 #include "../../include/moe_attn.h"
 #include "attn.hpp"
 #include "attn_decode.hpp"
+#include "attn_prefill.hpp"
 #include "attn_prepare.hpp"
-#include "attn_simple.hpp"
 
 namespace {
 
@@ -172,7 +172,8 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
   }
   return with_dim(c->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    return launch(k_attn_row<D>, dim3(static_cast<unsigned>(B * max_q * c->n_heads)), dim3(64), s, a);
+    const int64_t blocks = cdiv(max_q * a.group, PrefillShape<D>::COLS) * B * a.kv_heads;
+    return launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), s, a);
   });
 }
 
