@@ -28,8 +28,9 @@ constexpr int PF_TS = 64;            // keys of a tile
 
 template <int D>
 struct PrefillShape {
-  static constexpr int CT = D == 256 ? 1 : 2;
-  static constexpr int COLS = 4 * 32 * CT;
+  static constexpr int CT = 1;
+  static constexpr int NW = D == 256 ? 4 : 8;
+  static constexpr int COLS = NW * 32 * CT;
 };
 
 // Weights may exceed the running maximum by this many powers of two before
@@ -37,8 +38,8 @@ struct PrefillShape {
 constexpr float PF_SLACK = 8.0f;
 
 template <int D>
-__global__ __launch_bounds__(256, 1) void k_attn_prefill(AttnArgs a) {
-  constexpr int CT = PrefillShape<D>::CT, COLS = PrefillShape<D>::COLS, KS = D / 16, DT = D / 32;
+__global__ __launch_bounds__(PrefillShape<D>::NW * 64, 1) void k_attn_prefill(AttnArgs a) {
+  constexpr int NW = PrefillShape<D>::NW, CT = PrefillShape<D>::CT, COLS = PrefillShape<D>::COLS, KS = D / 16, DT = D / 32;
   constexpr int NSA = 2 * KS, NSB = 4 * DT;     // steps (of CT matrix instructions) of the two phases
   constexpr int NP = 16 * CT;                   // pairs of scores of a lane
   // pairs a step, and steps a pair
@@ -98,20 +99,21 @@ __global__ __launch_bounds__(256, 1) void k_attn_prefill(AttnArgs a) {
     const uint16_t* p = a.k + (static_cast<int64_t>(id) * a.kv_heads + kvh) * head_elems +
                         ((static_cast<int64_t>(w) << a.page_shift) + at) * 8;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + ((4 * i * 8) << a.page_shift)),
-                                       (lds_t*)(slot + (4 * i + w) * 64), 16, 0, 0);
+    for (int i = 0; i < D / 8 / NW; ++i)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + ((NW * i * 8) << a.page_shift)),
+                                       (lds_t*)(slot + (NW * i + w) * 64), 16, 0, 0);
   };
   // V slot: [8 groups of 8 keys][D][16 bytes]; wavefront w brings keys 16 w .. +15
   // (one page), whose page is that of the key that lane 16 w loads
   auto issue_v = [&](int v, int id, uint4* slot) __attribute__((always_inline)) {
-    const int at = (PF_TS * tl.tile(v) + 16 * w) & (ps - 1);
-    const int vid = __builtin_amdgcn_readlane(id, 16 * w);
+    constexpr int WK = PF_TS / NW;                // keys a wavefront brings
+    const int at = (PF_TS * tl.tile(v) + WK * w) & (ps - 1);
+    const int vid = __builtin_amdgcn_readlane(id, swap23(WK * w));
     const uint16_t* p = a.v + (static_cast<int64_t>(vid) * a.kv_heads + kvh) * head_elems + at * D + lane * 8;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + 512 * i), (lds_t*)(slot + 2 * D * w + 64 * i), 16,
-                                       0, 0);
+    for (int i = 0; i < D / 8 / NW; ++i)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + 512 * i), (lds_t*)(slot + D * 8 / NW * w + 64 * i),
+                                       16, 0, 0);
   };
   auto arrive = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_prefill(AttnArgs a) {
   auto clear_holes = [&](int v, uint4* slot) __attribute__((always_inline)) {
     const int key0 = PF_TS * tl.tile(v);
     if (key0 + PF_TS <= tl.hi && (key0 >= tl.lo || key0 + PF_TS <= tl.sinks)) return;
-    for (int i = tid; i < D * 8; i += 256) {
+    for (int i = tid; i < D * 8; i += NW * 64) {
       const int ka = key0 + 8 * (i / D);
       slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(visible_bits(ka, tl.hi - 1, tl.lo, tl.sinks))));
     }

@@ -173,7 +173,7 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
   return with_dim(c->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
     const int64_t blocks = cdiv(max_q * a.group, PrefillShape<D>::COLS) * B * a.kv_heads;
-    return launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), s, a);
+    return launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks)), dim3(PrefillShape<D>::NW * 64), s, a);
   });
 }
 
