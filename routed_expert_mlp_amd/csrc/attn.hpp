@@ -38,14 +38,19 @@ struct AttnSeq {
   int n, len;
 };
 
+// The same for every lane; said so, because values out of vector loads would
+// otherwise be kept, and worked on, in vector registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   AttnSeq s;
-  s.len = min(max(a.seq_lens[b], 0), a.max_len);
+  s.len = uniform(min(max(a.seq_lens[b], 0), a.max_len));
   if (a.cu_q) {
-    const int64_t r0 = min(max(static_cast<int64_t>(a.cu_q[b]), int64_t(0)), a.T);
-    const int64_t r1 = min(max(static_cast<int64_t>(a.cu_q[b + 1]), r0), a.T);
+    const int T = static_cast<int>(a.T);
+    const int r0 = uniform(min(max(a.cu_q[b], 0), T));
+    const int r1 = uniform(min(max(a.cu_q[b + 1], r0), T));
     s.row0 = r0;
-    s.n = static_cast<int>(min(r1 - r0, static_cast<int64_t>(a.n_q)));
+    s.n = min(r1 - r0, a.n_q);
   } else {
     s.row0 = static_cast<int64_t>(b) * a.n_q;
     s.n = a.n_q;

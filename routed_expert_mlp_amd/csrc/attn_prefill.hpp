@@ -1,36 +1,39 @@
 // Causal attention of prompts over the paged cache.
 //
 // What bounds it: 4 D flops per query head and visible key on the matrix
-// cores; the softmax's exponentials, conversions and sums on the vector units
-// take a little less time than that, so the two have to run at once.
-//   * A block is 4 wavefronts, one per SIMD with up to 512 registers, and 4 x
-//     32 CT columns (CT = 2, and 1 at 256 dims): the query rows of one
-//     key/value head, (new token, head of the group) with the head running
-//     faster, so that a key tile serves the whole group.  64 columns a
-//     wavefront halve the LDS reads per matrix instruction against 32: each
-//     operand fragment of K or V feeds two of them.
-//   * Tiles of 64 keys go from the cache to LDS by DMA, two slots for K and
-//     two for V, in the cache's own order: fragments are then consecutive 16
-//     bytes a lane, free of bank conflicts, and nothing is transposed.
+// cores; the softmax's exponentials, conversions and sums take the vector
+// units nearly as long, so the two have to run at once.
+//   * A wavefront owns 32 columns (query rows of one key/value head: new
+//     token x head of the group, the head running faster, so that a key tile
+//     serves the whole group) and a block NW of them.
+//   * Tiles of keys go from the cache to LDS by DMA, in rings of 4 slots for
+//     K and for V, in the cache's own order: operand fragments are then
+//     consecutive 16 bytes a lane, free of bank conflicts, and nothing is
+//     transposed.
 //   * Scores are computed transposed (attn.hpp), so the weights go from the
 //     softmax back into the matrix unit without leaving the lane.
 //   * One iteration computes the scores of tile t + 1 while the vector units
-//     turn those of tile t into weights, then adds tile t's weighted values
-//     while they look for tile t + 1's maximum; the sums are rescaled only
-//     when a maximum rises by more than 2^8.
+//     turn those of tile t into weights (phase A), then adds tile t's
+//     weighted values while they look for tile t + 1's maximum (phase B); the
+//     sums are rescaled only when a maximum rises by more than 2^8.
+//   * Fragments are read in groups of four, a group ahead of its use and
+//     across the barrier between the phases.
 #pragma once
 
 #include "attn.hpp"
 
+#include <type_traits>
+
 namespace moe {
 
-constexpr int PF_TS = 64;            // keys of a tile
+constexpr int PF_RING = 4;           // slots for keys, and as many for values
+constexpr int PF_IDS = 64;           // tiles whose page ids are in LDS, in two halves
 
 template <int D>
 struct PrefillShape {
-  static constexpr int CT = 1;
-  static constexpr int NW = D == 256 ? 4 : 8;
-  static constexpr int COLS = NW * 32 * CT;
+  static constexpr int TS = D == 256 ? 32 : 64;      // keys of a tile
+  static constexpr int NW = D == 128 ? 8 : 4;        // wavefronts of a block
+  static constexpr int COLS = 32 * NW;
 };
 
 // Weights may exceed the running maximum by this many powers of two before
@@ -38,12 +41,14 @@ struct PrefillShape {
 constexpr float PF_SLACK = 8.0f;
 
 template <int D>
-__global__ __launch_bounds__(PrefillShape<D>::NW * 64, 1) void k_attn_prefill(AttnArgs a) {
-  constexpr int NW = PrefillShape<D>::NW, CT = PrefillShape<D>::CT, COLS = PrefillShape<D>::COLS, KS = D / 16, DT = D / 32;
-  constexpr int NSA = 2 * KS, NSB = 4 * DT;     // steps (of CT matrix instructions) of the two phases
-  constexpr int NP = 16 * CT;                   // pairs of scores of a lane
-  // pairs a step, and steps a pair
-  constexpr int PA = NP > NSA ? NP / NSA : 1, SA = NP > NSA ? 1 : NSA / NP;
+__global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
+  constexpr int TS = PrefillShape<D>::TS, NW = PrefillShape<D>::NW, COLS = PrefillShape<D>::COLS;
+  constexpr int RING = PF_RING, KS = D / 16, DT = D / 32, SUB = TS / 32;
+  constexpr int NGA = SUB * KS / 4, NGB = 2 * SUB * DT / 4;      // groups of 4 matrix instructions of the two phases
+  static_assert(NGA % 2 == 0 && NGB % 2 == 0, "fragment buffers alternate");
+  constexpr int NP = 8 * SUB;                                    // pairs of scores of a lane
+  constexpr int NSA = 4 * NGA, NSB = 4 * NGB;                    // steps
+  constexpr int PA = NP > NSA ? NP / NSA : 1, SA = NP > NSA ? 1 : NSA / NP;   // pairs a step, steps a pair
   constexpr int PB = NP > NSB ? NP / NSB : 1, SB = NP > NSB ? 1 : NSB / NP;
   // key/value heads run fastest over the blocks: with a multiple of 8 of them
   // the blocks of one stay on one XCD, whose L2 then holds its keys; the
@@ -56,252 +61,274 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, 1) void k_attn_prefill(At
   const int cols = s.n * a.group;
   const int c0 = cb * COLS;
   if (c0 >= cols) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r = lane & 31, half = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
+  const int w = uniform(tid >> 6);
   const int first = s.len - s.n;
-  const int p_first = first + c0 / a.group, p_last = first + (min(c0 + COLS, cols) - 1) / a.group;
-  const AttnTiles tl = attn_tiles<PF_TS>(a, p_first, p_last);
+  const int p_first = uniform(first + c0 / a.group), p_last = uniform(first + (min(c0 + COLS, cols) - 1) / a.group);
+  const AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
 
-  __shared__ uint4 k0[D * 8], k1[D * 8], v0[D * 8], v1[D * 8];
+  // slots are arrays of their own, so that the compiler knows which reads a
+  // transfer in flight cannot touch
+  __shared__ uint4 k0[TS * D / 8], k1[TS * D / 8], k2[TS * D / 8], k3[TS * D / 8];
+  __shared__ uint4 v0[TS * D / 8], v1[TS * D / 8], v2[TS * D / 8], v3[TS * D / 8];
+  __shared__ int ids[TS / 16 * PF_IDS];          // pages of 16 keys each
+  uint4* const kslot[RING] = {k0, k1, k2, k3};
+  uint4* const vslot[RING] = {v0, v1, v2, v3};
 
-  // this lane's columns
-  int pos[CT], wlo[CT];
-  int64_t row[CT];
-  bf16x8 qf[CT][KS];
+  // this lane's column
+  const int col = min(c0 + 32 * w + r, cols - 1);
+  const int tok = col / a.group;
+  const int pos = first + tok, wlo = attn_window_lo(a, pos);
+  const int64_t row = (s.row0 + tok) * a.heads + kvh * a.group + (col - tok * a.group);
+  bf16x8 qf[KS];
+  {
+    const uint16_t* qp = a.q + row * D + 8 * half;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int col = min(c0 + 32 * (CT * w + ct) + r, cols - 1);
-    const int t = col / a.group;
-    pos[ct] = first + t;
-    wlo[ct] = attn_window_lo(a, pos[ct]);
-    row[ct] = (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
-    const uint16_t* qp = a.q + row[ct] * D + 8 * half;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) qf[ct][ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
+    for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
   }
-  // of this wavefront's columns, the first and last position and the last window start
-  const int wp_first = first + min(c0 + 32 * CT * w, cols - 1) / a.group;
-  const int wp_last = first + min(c0 + 32 * CT * (w + 1) - 1, cols - 1) / a.group;
-  const int wlo_last = attn_window_lo(a, wp_last);
+  // of this wavefront's columns, the first position and the last window start
+  const int wp_first = uniform(first + min(c0 + 32 * w, cols - 1) / a.group);
+  const int wlo_last = attn_window_lo(a, uniform(first + min(c0 + 32 * w + 31, cols - 1) / a.group));
 
   const int ps = 1 << a.page_shift;
-  const int64_t head_elems = static_cast<int64_t>(D) << a.page_shift;
-  // Key of the tile that this lane loads (row l of the K slot holds key
-  // swap23(l % 32) of its half), and its page.
-  const int lkey = 32 * half + swap23(r);
-  auto page_of = [&](int v) __attribute__((always_inline)) {
-    const int key = min(PF_TS * tl.tile(min(v, tl.n - 1)) + lkey, s.len - 1);
-    return min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
+  const uint32_t head_bytes = static_cast<uint32_t>(2 * D) << a.page_shift;
+  const uint32_t page_bytes = head_bytes * a.kv_heads;
+  // Pages of tiles v0 .. v0 + n - 1 to their places of `ids`.
+  auto load_ids = [&](int first_tile, int n) __attribute__((always_inline)) {
+    for (int i = tid; i < TS / 16 * n; i += NW * 64) {
+      const int v = first_tile + i / (TS / 16), part = i % (TS / 16);
+      const int key = min(TS * tl.tile(min(v, tl.n - 1)) + 16 * part, s.len - 1);
+      ids[TS / 16 * (v % PF_IDS) + part] =
+          min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);          // the writes have been done (lgkmcnt 0)
   };
   using lds_t = void __attribute__((address_space(3)));
-  // K slot: [D / 8][64 keys][16 bytes]; wavefront w brings every fourth row
-  auto issue_k = [&](int v, int id, uint4* slot) __attribute__((always_inline)) {
-    const int at = (PF_TS * tl.tile(v) + lkey) & (ps - 1);
-    const uint16_t* p = a.k + (static_cast<int64_t>(id) * a.kv_heads + kvh) * head_elems +
-                        ((static_cast<int64_t>(w) << a.page_shift) + at) * 8;
+  constexpr int NI = TS * D / 8 / 64 / NW;       // transfers of a wavefront for a tile's keys, and for its values
+  // K slot: [D / 8][TS keys][16 bytes], row l of it key swap23(l % 32) of its 32
+  constexpr int CPI = 64 / TS;                   // chunks of 8 dims a transfer
+  const int lkey = TS == 64 ? 32 * half + swap23(r) : swap23(r);
+  const int lchunk = CPI * w + (TS == 64 ? 0 : half);
+  const uint64_t kbase = reinterpret_cast<uint64_t>(a.k) + static_cast<uint64_t>(kvh) * head_bytes +
+                         ((lchunk << a.page_shift) + (lkey & (ps - 1))) * 16;
+  auto issue_k = [&](int v, uint4* slot) __attribute__((always_inline)) {
+    const uint32_t id = ids[TS / 16 * (v % PF_IDS) + (lkey >> 4)];
+    const uint64_t p = static_cast<uint64_t>(id) * page_bytes + kbase +
+                       static_cast<uint32_t>((TS * tl.tile(v)) & (ps - 1)) * 16;
 #pragma unroll
-    for (int i = 0; i < D / 8 / NW; ++i)
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + ((NW * i * 8) << a.page_shift)),
+    for (int i = 0; i < NI; ++i)
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
                                        (lds_t*)(slot + (NW * i + w) * 64), 16, 0, 0);
   };
-  // V slot: [8 groups of 8 keys][D][16 bytes]; wavefront w brings keys 16 w .. +15
-  // (one page), whose page is that of the key that lane 16 w loads
-  auto issue_v = [&](int v, int id, uint4* slot) __attribute__((always_inline)) {
-    constexpr int WK = PF_TS / NW;                // keys a wavefront brings
-    const int at = (PF_TS * tl.tile(v) + WK * w) & (ps - 1);
-    const int vid = __builtin_amdgcn_readlane(id, swap23(WK * w));
-    const uint16_t* p = a.v + (static_cast<int64_t>(vid) * a.kv_heads + kvh) * head_elems + at * D + lane * 8;
+  // V slot: [TS / 8][D][16 bytes]; wavefront w brings keys TS / NW * w and on, all of one page
+  constexpr int WK = TS / NW;
+  const uint64_t vbase = reinterpret_cast<uint64_t>(a.v) + static_cast<uint64_t>(kvh) * head_bytes +
+                         ((WK * w) & (ps - 1)) * (2 * D) + lane * 16;
+  auto issue_v = [&](int v, uint4* slot) __attribute__((always_inline)) {
+    const uint32_t id = uniform(ids[TS / 16 * (v % PF_IDS) + (WK * w >> 4)]);
+    const uint64_t p = static_cast<uint64_t>(id) * page_bytes + vbase +
+                       static_cast<uint32_t>((TS * tl.tile(v)) & (ps - 1)) * (2 * D);
 #pragma unroll
-    for (int i = 0; i < D / 8 / NW; ++i)
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + 512 * i), (lds_t*)(slot + D * 8 / NW * w + 64 * i),
-                                       16, 0, 0);
+    for (int i = 0; i < NI; ++i)
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
+                                       (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
   };
-  auto arrive = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  // Waits for this wavefront's transfers but the VM latest (all, unless
+  // `steady`), then for the other wavefronts to be here too.
+  auto arrive = [&](auto vm, bool steady) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
+    if (steady) __builtin_amdgcn_s_waitcnt(waitcnt_vm(decltype(vm)::value));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 
-  f32x16 acc[CT][DT], sa[2][CT], sb[2][CT];
-  float m[CT], l[CT];
+  f32x16 acc[DT], sa[SUB], sb[SUB];
+  float m = ATTN_NO_MAX, l = 0.0f;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    m[ct] = ATTN_NO_MAX;
-    l[ct] = 0.0f;
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[dt][e] = 0.0f;
+
+  // scores of invisible keys to -inf, where the tile has some for this wavefront
+  auto mask = [&](int v, f32x16 (&x)[SUB]) __attribute__((always_inline)) {
+    const int key0 = TS * tl.tile(v);
+    if (key0 + TS - 1 <= wp_first && (key0 >= wlo_last || key0 + TS <= tl.sinks)) return;
+    const uint64_t see = visible_bits(key0 + 8 * half, pos, wlo, tl.sinks);
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x[sub][e] = keep_if(static_cast<uint32_t>(see >> (32 * sub)), 16 * (e >> 3) + (e & 7), x[sub][e]);
+  };
+  // new maximum (mx: this lane's largest score), and the sums rescaled if it rose enough
+  auto rescale = [&](float mx) __attribute__((always_inline)) {
+    const float mt = max_halves(mx) * a.scale_log2;
+    if (!__any(mt > m + PF_SLACK)) return;
+    const float mn = fmaxf(m, mt);
+    const float f = exp2_fast(m - mn);
+    m = mn;
+    l *= f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[ct][dt][e] = 0.0f;
-  }
-
-  // scores of invisible keys to -inf, where the tile has some for this wavefront
-  auto mask = [&](int v, f32x16 (&x)[2][CT]) __attribute__((always_inline)) {
-    const int key0 = PF_TS * tl.tile(v);
-    if (key0 + PF_TS - 1 <= wp_first && (key0 >= wlo_last || key0 + PF_TS <= tl.sinks)) return;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const uint64_t see = visible_bits(key0 + 8 * half, pos[ct], wlo[ct], tl.sinks);
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          x[sub][ct][e] = keep_if(static_cast<uint32_t>(see >> (32 * sub)), 16 * (e >> 3) + (e & 7), x[sub][ct][e]);
-    }
-  };
-  // new maxima (mx: this lane's largest scores), and the sums rescaled if one rose enough
-  auto rescale = [&](const float (&mx)[CT]) __attribute__((always_inline)) {
-    float mt[CT];
-    bool up = false;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      mt[ct] = max_halves(mx[ct]) * a.scale_log2;
-      up |= mt[ct] > m[ct] + PF_SLACK;
-    }
-    if (!__any(up)) return;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const float mn = fmaxf(m[ct], mt[ct]);
-      const float f = exp2_fast(m[ct] - mn);
-      m[ct] = mn;
-      l[ct] *= f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[ct][dt][e] *= f;
-    }
+      for (int e = 0; e < 16; ++e) acc[dt][e] *= f;
   };
   // values of keys that no column sees, whatever their slots hold, to 0 (all wavefronts)
   auto clear_holes = [&](int v, uint4* slot) __attribute__((always_inline)) {
-    const int key0 = PF_TS * tl.tile(v);
-    if (key0 + PF_TS <= tl.hi && (key0 >= tl.lo || key0 + PF_TS <= tl.sinks)) return;
-    for (int i = tid; i < D * 8; i += NW * 64) {
-      const int ka = key0 + 8 * (i / D);
-      slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(visible_bits(ka, tl.hi - 1, tl.lo, tl.sinks))));
-    }
+    const int key0 = TS * tl.tile(v);
+    if (key0 + TS <= tl.hi && (key0 >= tl.lo || key0 + TS <= tl.sinks)) return;
+    for (int i = tid; i < TS * D / 8; i += NW * 64)
+      slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(visible_bits(key0 + 8 * (i / D), tl.hi - 1, tl.lo, tl.sinks))));
     __syncthreads();
   };
-  auto kfrag = [&](const uint4* slot, int step) __attribute__((always_inline)) {          // step = sub * KS + ks
-    return __builtin_bit_cast(bf16x8, slot[(2 * (step % KS) + half) * 64 + 32 * (step / KS) + r]);
-  };
-  auto vfrag = [&](const uint4* slot, int step) __attribute__((always_inline)) {          // step = 16 keys * DT + dt
-    return __builtin_bit_cast(bf16x8, slot[(2 * (step / DT) + half) * D + 32 * (step % DT) + r]);
-  };
-
-  // One iteration: weights and values of tile v, scores of tile v + 1.
-  // kn: slot of tile v + 1's keys; kf: slot for tile v + 2's; vc: slot of
-  // tile v's values; vf: slot for tile v + 1's.  id1, id2: pages of tiles
-  // v + 1 and v + 2.
-  auto iteration = [&](int v, f32x16 (&sc)[2][CT], f32x16 (&sn)[2][CT], const uint4* kn, uint4* kf, uint4* vc, uint4* vf, int id1, int id2) __attribute__((always_inline)) {
-    arrive();
-    if (v + 2 < tl.n) issue_k(v + 2, id2, kf);
-    if (v + 1 < tl.n) issue_v(v + 1, id1, vf);
-    clear_holes(v, vc);
-    uint32_t pk[CT][4][4];
-    constexpr int AHEAD = 3;
-    bf16x8 fr[AHEAD];
+  // Group g of 4 fragments of a K slot (32 keys, then 16 dims on) or V slot (16 keys, then 32 dims on).
+  bf16x8 fr[2][4];
+  auto read_k = [&](const uint4* slot, int g, bf16x8 (&f)[4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fr[i] = kfrag(kn, i);
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * g + j;
+      f[j] = __builtin_bit_cast(bf16x8, slot[(2 * (i % KS) + half) * TS + 32 * (i / KS) + r]);
+    }
+  };
+  auto read_v = [&](const uint4* slot, int g, bf16x8 (&f)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * g + j;
+      f[j] = __builtin_bit_cast(bf16x8, slot[(2 * (i / DT) + half) * D + 32 * (i % DT) + r]);
+    }
+  };
+  // Pair p of the scores to weights, their sum to l.
+  uint32_t pk[2 * SUB][4];
+  auto weigh = [&](int p, const f32x16 (&x)[SUB]) __attribute__((always_inline)) {
+    const int su = p >> 3, e = 2 * (p & 7);
+    const float p0 = exp2_fast(fmaf(x[su][e], a.scale_log2, -m));
+    const float p1 = exp2_fast(fmaf(x[su][e + 1], a.scale_log2, -m));
+    uint32_t pp = pack_bf16x2(p0, p1);
+    l = dot2_bf16(pp, 0x3F803F80u, l);
+    asm volatile("" : "+v"(pp), "+v"(l));        // here, beside the matrix instructions, and not where it is used
+    pk[2 * su + (e >> 3)][(e & 7) >> 1] = pp;
+  };
+  auto weights = [&](int kk) __attribute__((always_inline)) {
+    return __builtin_bit_cast(bf16x8, uint4{pk[kk][0], pk[kk][1], pk[kk][2], pk[kk][3]});
+  };
+  // After everyone's phase A of tile t: transfers into the slots that nobody
+  // reads any more; the keys of tile t + 2 and the values of t + 1 are there.
+  auto middle = [&](auto jc, int t) __attribute__((always_inline)) {
+    constexpr int J = decltype(jc)::value;       // (t + RING) % RING
+    arrive(std::integral_constant<int, 3 * NI>{}, t + RING < tl.n);
+    if (t >= 0 && t - 1 + RING < tl.n) issue_v(t - 1 + RING, vslot[(J + RING - 1) % RING]);
+    if (t < 0 && RING - 2 < tl.n) issue_v(RING - 2, vslot[RING - 2]);
+    if (t + 1 + RING < tl.n) issue_k(t + 1 + RING, kslot[(J + 1) % RING]);
+    clear_holes(t + 1, vslot[(J + 1) % RING]);
+  };
+  // Phases A and B of tile t; x: its scores, y: those of tile t + 1.
+  auto iteration = [&](auto jc, int t, f32x16 (&x)[SUB], f32x16 (&y)[SUB]) __attribute__((always_inline)) {
+    constexpr int J = decltype(jc)::value;       // t % RING
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
-      const int sub = i / KS, ks = i % KS;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        f32x16 z = {};
-        sn[sub][ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % AHEAD], qf[ct][ks], ks == 0 ? z : sn[sub][ct], 0, 0, 0);
+      const int g = i / 4, sub = i / KS;
+      f32x16 z = {};
+      y[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], qf[i % KS], i % KS ? y[sub] : z, 0, 0, 0);
+      if (i % 4 == 0) {
+        if (g + 1 < NGA) read_k(kslot[(J + 1) % RING], g + 1, fr[(g + 1) & 1]);
+        else read_v(vslot[J], 0, fr[0]);
       }
-      if (i + AHEAD < NSA) fr[i % AHEAD] = kfrag(kn, i + AHEAD);
 #pragma unroll
-      for (int j = 0; j < PA; ++j) {
-        if (i % SA) break;
-        const int p = i / SA * PA + j;
-        const int ct = p % CT, q = p / CT, su = q >> 3, e = 2 * (q & 7);   // pair of tile v's scores
-        const float p0 = exp2_fast(fmaf(sc[su][ct][e], a.scale_log2, -m[ct]));
-        const float p1 = exp2_fast(fmaf(sc[su][ct][e + 1], a.scale_log2, -m[ct]));
-        l[ct] += p0 + p1;
-        pk[ct][2 * su + (e >> 3)][(e & 7) >> 1] = pack_bf16x2(p0, p1);
-      }
+      for (int j = 0; j < PA; ++j)
+        if (i % SA == 0) weigh(i / SA * PA + j, x);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (v + 1 < tl.n) mask(v + 1, sn);
-    float mx[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) mx[ct] = sn[0][ct][0];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fr[i] = vfrag(vc, i);
+    middle(jc, t);
+    mask(t + 1, y);
+    float mx = y[0][0];
 #pragma unroll
     for (int i = 0; i < NSB; ++i) {
-      const int kk = i / DT, dt = i % DT;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const uint4 pf = {pk[ct][kk][0], pk[ct][kk][1], pk[ct][kk][2], pk[ct][kk][3]};
-        acc[ct][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % AHEAD], __builtin_bit_cast(bf16x8, pf), acc[ct][dt], 0, 0, 0);
+      const int g = i / 4;
+      acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], weights(i / DT), acc[i % DT], 0, 0, 0);
+      if (i % 4 == 0) {
+        if (g + 1 < NGB) read_v(vslot[J], g + 1, fr[(g + 1) & 1]);
+        else read_k(kslot[(J + 2) % RING], 0, fr[0]);
       }
-      if (i + AHEAD < NSB) fr[i % AHEAD] = vfrag(vc, i + AHEAD);
 #pragma unroll
-      for (int j = 0; j < PB; ++j) {
-        if (i % SB) break;
-        const int p = i / SB * PB + j;
-        const int ct = p % CT, q = p / CT, su = q >> 3, e = 2 * (q & 7);
-        mx[ct] = fmaxf(fmaxf(mx[ct], sn[su][ct][e]), sn[su][ct][e + 1]);
-      }
+      for (int j = 0; j < PB; ++j)
+        if (i % SB == 0) {
+          const int p = i / SB * PB + j, su = p >> 3, e = 2 * (p & 7);
+          mx = fmaxf(fmaxf(mx, y[su][e]), y[su][e + 1]);
+          asm volatile("" : "+v"(mx));
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (v + 1 < tl.n) rescale(mx);
+    rescale(mx);
   };
 
   if (tl.n > 0) {
-    int ida = page_of(0), idb = page_of(1);
-    issue_k(0, ida, k0);
-    issue_v(0, ida, v0);
-    if (tl.n > 1) issue_k(1, idb, k1);
-    arrive();
+    load_ids(0, PF_IDS);
+    __syncthreads();
+    issue_k(0, k0);
+    if (1 < tl.n) issue_k(1, k1);
+    issue_v(0, v0);
+    if (2 < tl.n) issue_k(2, k2);
+    if (1 < tl.n) issue_v(1, v1);
+    if (3 < tl.n) issue_k(3, k3);
+    arrive(std::integral_constant<int, 5 * NI>{}, 3 < tl.n);
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
-      const int sub = i / KS, ks = i % KS;
-      const bf16x8 f = kfrag(k0, i);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        f32x16 z = {};
-        sa[sub][ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[ct][ks], ks == 0 ? z : sa[sub][ct], 0, 0, 0);
-      }
+      f32x16 z = {};
+      const bf16x8 f = __builtin_bit_cast(bf16x8, k0[(2 * (i % KS) + half) * TS + 32 * (i / KS) + r]);
+      sa[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[i % KS], i % KS ? sa[i / KS] : z, 0, 0, 0);
     }
     mask(0, sa);
-    float mx[CT];
+    float mx = sa[0][0];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      mx[ct] = sa[0][ct][0];
+    for (int su = 0; su < SUB; ++su)
 #pragma unroll
-      for (int su = 0; su < 2; ++su)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mx[ct] = fmaxf(mx[ct], sa[su][ct][e]);
-    }
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
     rescale(mx);
-    for (int v = 0; v < tl.n; v += 2) {
-      // page of tile v + 2 was asked for two tiles ago, in the shadow of the work since
-      const int idc = page_of(v + 2);
-      iteration(v, sa, sb, k1, k0, v0, v1, idb, idc);
-      ida = idc;
-      if (v + 1 >= tl.n) break;
-      idb = page_of(v + 3);
-      iteration(v + 1, sb, sa, k0, k1, v1, v0, ida, idb);
+    middle(std::integral_constant<int, RING - 1>{}, -1);
+    read_k(k1, 0, fr[0]);
+    const int last = tl.n - 1;
+    for (int t = 0; t < last; t += RING) {
+      if (t % (PF_IDS / 2) == 0 && t) load_ids(t + PF_IDS / 2, PF_IDS / 2);
+      iteration(std::integral_constant<int, 0>{}, t, sa, sb);
+      if (t + 1 >= last) break;
+      iteration(std::integral_constant<int, 1>{}, t + 1, sb, sa);
+      if (t + 2 >= last) break;
+      iteration(std::integral_constant<int, 2>{}, t + 2, sa, sb);
+      if (t + 3 >= last) break;
+      iteration(std::integral_constant<int, 3>{}, t + 3, sb, sa);
+    }
+    // the last tile's weights and values
+    if (last & 1) {
+#pragma unroll
+      for (int su = 0; su < SUB; ++su) sa[su] = sb[su];
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) weigh(p, sa);
+    const int j = last % RING;
+    const uint4* vl = j == 0 ? v0 : j == 1 ? v1 : j == 2 ? v2 : v3;
+#pragma unroll
+    for (int g = 0; g < NGB; ++g) {
+      read_v(vl, g, fr[g & 1]);
+#pragma unroll
+      for (int i = 4 * g; i < 4 * g + 4; ++i)
+        acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], weights(i / DT), acc[i % DT], 0, 0, 0);
     }
   }
 
+  const float lt = sum_halves(l);
+  const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+  if (c0 + 32 * w + r >= cols) return;
+  uint16_t* o = a.out + row * D + 4 * half;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const float lt = sum_halves(l[ct]);
-    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-    if (c0 + 32 * (CT * w + ct) + r >= cols) continue;
-    uint16_t* o = a.out + row[ct] * D + 4 * half;
+  for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint2 p = {pack_bf16x2(acc[ct][dt][4 * i] * inv, acc[ct][dt][4 * i + 1] * inv),
-                         pack_bf16x2(acc[ct][dt][4 * i + 2] * inv, acc[ct][dt][4 * i + 3] * inv)};
-        *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
-      }
-  }
+    for (int i = 0; i < 4; ++i) {
+      const uint2 p = {pack_bf16x2(acc[dt][4 * i] * inv, acc[dt][4 * i + 1] * inv),
+                       pack_bf16x2(acc[dt][4 * i + 2] * inv, acc[dt][4 * i + 3] * inv)};
+      *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
+    }
 }
 
 }  // namespace moe
