@@ -26,7 +26,8 @@
 
 namespace moe {
 
-constexpr int PF_RING = 4;           // slots for keys, and as many for values
+constexpr int PF_RING = 4;           // slots for values
+constexpr int PF_KRING = 2;          // slots for keys
 constexpr int PF_IDS = 64;           // tiles whose page ids are in LDS, in two halves
 
 template <int D>
@@ -43,7 +44,7 @@ constexpr float PF_SLACK = 8.0f;
 template <int D>
 __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
   constexpr int TS = PrefillShape<D>::TS, NW = PrefillShape<D>::NW, COLS = PrefillShape<D>::COLS;
-  constexpr int RING = PF_RING, KS = D / 16, DT = D / 32, SUB = TS / 32;
+  constexpr int RING = PF_RING, KRING = PF_KRING, KS = D / 16, DT = D / 32, SUB = TS / 32;
   constexpr int NGA = SUB * KS / 4, NGB = 2 * SUB * DT / 4;      // groups of 4 matrix instructions of the two phases
   static_assert(NGA % 2 == 0 && NGB % 2 == 0, "fragment buffers alternate");
   constexpr int NP = 8 * SUB;                                    // pairs of scores of a lane
@@ -69,10 +70,10 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 
   // slots are arrays of their own, so that the compiler knows which reads a
   // transfer in flight cannot touch
-  __shared__ uint4 k0[TS * D / 8], k1[TS * D / 8], k2[TS * D / 8], k3[TS * D / 8];
+  __shared__ uint4 k0[TS * D / 8], k1[TS * D / 8];
   __shared__ uint4 v0[TS * D / 8], v1[TS * D / 8], v2[TS * D / 8], v3[TS * D / 8];
   __shared__ int ids[TS / 16 * PF_IDS];          // pages of 16 keys each
-  uint4* const kslot[RING] = {k0, k1, k2, k3};
+  uint4* const kslot[KRING] = {k0, k1};
   uint4* const vslot[RING] = {v0, v1, v2, v3};
 
   // this lane's column
@@ -112,10 +113,12 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   const int lchunk = CPI * w + (TS == 64 ? 0 : half);
   const uint64_t kbase = reinterpret_cast<uint64_t>(a.k) + static_cast<uint64_t>(kvh) * head_bytes +
                          ((lchunk << a.page_shift) + (lkey & (ps - 1))) * 16;
-  auto issue_k = [&](int v, uint4* slot) __attribute__((always_inline)) {
-    const uint32_t id = ids[TS / 16 * (v % PF_IDS) + (lkey >> 4)];
-    const uint64_t p = static_cast<uint64_t>(id) * page_bytes + kbase +
-                       static_cast<uint32_t>((TS * tl.tile(v)) & (ps - 1)) * 16;
+  auto key_source = [&](int v) __attribute__((always_inline)) {
+    const int vt = min(v, tl.n - 1);
+    const uint32_t id = ids[TS / 16 * (vt % PF_IDS) + (lkey >> 4)];
+    return static_cast<uint64_t>(id) * page_bytes + kbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * 16;
+  };
+  auto issue_k = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
@@ -125,21 +128,22 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   constexpr int WK = TS / NW;
   const uint64_t vbase = reinterpret_cast<uint64_t>(a.v) + static_cast<uint64_t>(kvh) * head_bytes +
                          ((WK * w) & (ps - 1)) * (2 * D) + lane * 16;
-  auto issue_v = [&](int v, uint4* slot) __attribute__((always_inline)) {
-    const uint32_t id = uniform(ids[TS / 16 * (v % PF_IDS) + (WK * w >> 4)]);
-    const uint64_t p = static_cast<uint64_t>(id) * page_bytes + vbase +
-                       static_cast<uint32_t>((TS * tl.tile(v)) & (ps - 1)) * (2 * D);
+  auto value_source = [&](int v) __attribute__((always_inline)) {
+    const int vt = min(v, tl.n - 1);
+    const uint32_t id = uniform(ids[TS / 16 * (vt % PF_IDS) + (WK * w >> 4)]);
+    return static_cast<uint64_t>(id) * page_bytes + vbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * (2 * D);
+  };
+  auto issue_v = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
                                        (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
   };
-  // Waits for this wavefront's transfers but the VM latest (all, unless
-  // `steady`), then for the other wavefronts to be here too.
-  auto arrive = [&](auto vm, bool steady) __attribute__((always_inline)) {
+  // Waits for this wavefront's transfers but the VM latest, then for the other
+  // wavefronts to be here too.
+  auto arrive = [&](auto vm) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
-    if (steady) __builtin_amdgcn_s_waitcnt(waitcnt_vm(decltype(vm)::value));
-    else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(decltype(vm)::value));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -213,34 +217,32 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   auto weights = [&](int kk) __attribute__((always_inline)) {
     return __builtin_bit_cast(bf16x8, uint4{pk[kk][0], pk[kk][1], pk[kk][2], pk[kk][3]});
   };
-  // After everyone's phase A of tile t: transfers into the slots that nobody
-  // reads any more; the keys of tile t + 2 and the values of t + 1 are there.
-  auto middle = [&](auto jc, int t) __attribute__((always_inline)) {
-    constexpr int J = decltype(jc)::value;       // (t + RING) % RING
-    arrive(std::integral_constant<int, 3 * NI>{}, t + RING < tl.n);
-    if (t >= 0 && t - 1 + RING < tl.n) issue_v(t - 1 + RING, vslot[(J + RING - 1) % RING]);
-    if (t < 0 && RING - 2 < tl.n) issue_v(RING - 2, vslot[RING - 2]);
-    if (t + 1 + RING < tl.n) issue_k(t + 1 + RING, kslot[(J + 1) % RING]);
-    clear_holes(t + 1, vslot[(J + 1) % RING]);
-  };
-  // Phases A and B of tile t; x: its scores, y: those of tile t + 1.
+  // Phases A and B of tile t; x: its scores, y: those of tile t + 1.  Between
+  // the two, everyone is past its reads of the keys of tile t + 1 and the
+  // values of tile t - 1, whose slots take the keys of t + 3 and the values of
+  // t + 3 (past the end the last tile again, which nobody reads); the keys of
+  // tile t + 2 and the values of t + 1 have come.
   auto iteration = [&](auto jc, int t, f32x16 (&x)[SUB], f32x16 (&y)[SUB]) __attribute__((always_inline)) {
     constexpr int J = decltype(jc)::value;       // t % RING
+    uint64_t ksrc = 0, vsrc = 0;
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
       const int g = i / 4, sub = i / KS;
       f32x16 z = {};
       y[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], qf[i % KS], i % KS ? y[sub] : z, 0, 0, 0);
       if (i % 4 == 0) {
-        if (g + 1 < NGA) read_k(kslot[(J + 1) % RING], g + 1, fr[(g + 1) & 1]);
+        if (g + 1 < NGA) read_k(kslot[(J + 1) % KRING], g + 1, fr[(g + 1) & 1]);
         else read_v(vslot[J], 0, fr[0]);
       }
 #pragma unroll
       for (int j = 0; j < PA; ++j)
         if (i % SA == 0) weigh(i / SA * PA + j, x);
+      if (i == 1) ksrc = key_source(t + 3);
+      if (i == 2) vsrc = value_source(t + 3);
       __builtin_amdgcn_sched_barrier(0);
     }
-    middle(jc, t);
+    arrive(std::integral_constant<int, NI>{});
+    clear_holes(t + 1, vslot[(J + 1) % RING]);
     mask(t + 1, y);
     float mx = y[0][0];
 #pragma unroll
@@ -249,8 +251,10 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], weights(i / DT), acc[i % DT], 0, 0, 0);
       if (i % 4 == 0) {
         if (g + 1 < NGB) read_v(vslot[J], g + 1, fr[(g + 1) & 1]);
-        else read_k(kslot[(J + 2) % RING], 0, fr[0]);
+        else read_k(kslot[J % KRING], 0, fr[0]);
       }
+      if (i == 1) issue_k(ksrc, kslot[(J + 1) % KRING]);
+      if (i == 2) issue_v(vsrc, vslot[(J + 3) % RING]);
 #pragma unroll
       for (int j = 0; j < PB; ++j)
         if (i % SB == 0) {
@@ -266,13 +270,12 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   if (tl.n > 0) {
     load_ids(0, PF_IDS);
     __syncthreads();
-    issue_k(0, k0);
-    if (1 < tl.n) issue_k(1, k1);
-    issue_v(0, v0);
-    if (2 < tl.n) issue_k(2, k2);
-    if (1 < tl.n) issue_v(1, v1);
-    if (3 < tl.n) issue_k(3, k3);
-    arrive(std::integral_constant<int, 5 * NI>{}, 3 < tl.n);
+    issue_k(key_source(0), k0);
+    issue_k(key_source(1), k1);
+    issue_v(value_source(0), v0);
+    issue_v(value_source(1), v1);
+    const uint64_t ksrc = key_source(2), vsrc = value_source(2);
+    arrive(std::integral_constant<int, 3 * NI>{});
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
       f32x16 z = {};
@@ -286,7 +289,10 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
     rescale(mx);
-    middle(std::integral_constant<int, RING - 1>{}, -1);
+    arrive(std::integral_constant<int, NI>{});
+    issue_k(ksrc, k0);
+    issue_v(vsrc, v2);
+    clear_holes(0, v0);
     read_k(k1, 0, fr[0]);
     const int last = tl.n - 1;
     for (int t = 0; t < last; t += RING) {
@@ -299,7 +305,8 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       if (t + 3 >= last) break;
       iteration(std::integral_constant<int, 3>{}, t + 3, sb, sa);
     }
-    // the last tile's weights and values
+    // the last tile's weights and values; transfers end before the block gives up its LDS
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     if (last & 1) {
 #pragma unroll
       for (int su = 0; su < SUB; ++su) sa[su] = sb[su];
