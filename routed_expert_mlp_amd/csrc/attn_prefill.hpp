@@ -118,11 +118,9 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
     const uint32_t id = ids[TS / 16 * (vt % PF_IDS) + (lkey >> 4)];
     return static_cast<uint64_t>(id) * page_bytes + kbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * 16;
   };
-  auto issue_k = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
-                                       (lds_t*)(slot + (NW * i + w) * 64), 16, 0, 0);
+  auto issue_k = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
+                                     (lds_t*)(slot + (NW * i + w) * 64), 16, 0, 0);
   };
   // V slot: [TS / 8][D][16 bytes]; wavefront w brings keys TS / NW * w and on, all of one page
   constexpr int WK = TS / NW;
@@ -133,11 +131,17 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
     const uint32_t id = uniform(ids[TS / 16 * (vt % PF_IDS) + (WK * w >> 4)]);
     return static_cast<uint64_t>(id) * page_bytes + vbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * (2 * D);
   };
-  auto issue_v = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
+  auto issue_v = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
+                                     (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
+  };
+  auto all_k = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
-                                       (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
+    for (int i = 0; i < NI; ++i) issue_k(p, slot, i);
+  };
+  auto all_v = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) issue_v(p, slot, i);
   };
   // Waits for this wavefront's transfers but the VM latest, then for the other
   // wavefronts to be here too.
@@ -169,7 +173,7 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   // new maximum (mx: this lane's largest score), and the sums rescaled if it rose enough
   auto rescale = [&](float mx) __attribute__((always_inline)) {
     const float mt = max_halves(mx) * a.scale_log2;
-    if (!__any(mt > m + PF_SLACK)) return;
+    if (__builtin_expect(!__any(mt > m + PF_SLACK), 1)) return;
     const float mn = fmaxf(m, mt);
     const float f = exp2_fast(m - mn);
     m = mn;
@@ -222,6 +226,9 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   // values of tile t - 1, whose slots take the keys of t + 3 and the values of
   // t + 3 (past the end the last tile again, which nobody reads); the keys of
   // tile t + 2 and the values of t + 1 have come.
+  // tiles inner0 .. inner1 - 1 are visible as a whole to every column
+  const int inner0 = uniform(max(0, (attn_window_lo(a, p_last) + TS - 1) / TS - tl.b0) + tl.na);
+  const int inner1 = uniform(p_first < 0 ? 0 : (p_first + 1) / TS - tl.b0 + tl.na);
   auto iteration = [&](auto jc, int t, f32x16 (&x)[SUB], f32x16 (&y)[SUB]) __attribute__((always_inline)) {
     constexpr int J = decltype(jc)::value;       // t % RING
     uint64_t ksrc = 0, vsrc = 0;
@@ -242,8 +249,10 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       __builtin_amdgcn_sched_barrier(0);
     }
     arrive(std::integral_constant<int, NI>{});
-    clear_holes(t + 1, vslot[(J + 1) % RING]);
-    mask(t + 1, y);
+    if (__builtin_expect(t + 1 < inner0 || t + 1 >= inner1, 0)) {
+      clear_holes(t + 1, vslot[(J + 1) % RING]);
+      mask(t + 1, y);
+    }
     float mx = y[0][0];
 #pragma unroll
     for (int i = 0; i < NSB; ++i) {
@@ -253,8 +262,8 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
         if (g + 1 < NGB) read_v(vslot[J], g + 1, fr[(g + 1) & 1]);
         else read_k(kslot[J % KRING], 0, fr[0]);
       }
-      if (i == 1) issue_k(ksrc, kslot[(J + 1) % KRING]);
-      if (i == 2) issue_v(vsrc, vslot[(J + 3) % RING]);
+      if (i >= 1 && i <= NI) issue_k(ksrc, kslot[(J + 1) % KRING], i - 1);
+      if (i > NI && i <= 2 * NI) issue_v(vsrc, vslot[(J + 3) % RING], i - NI - 1);
 #pragma unroll
       for (int j = 0; j < PB; ++j)
         if (i % SB == 0) {
@@ -270,10 +279,10 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   if (tl.n > 0) {
     load_ids(0, PF_IDS);
     __syncthreads();
-    issue_k(key_source(0), k0);
-    issue_k(key_source(1), k1);
-    issue_v(value_source(0), v0);
-    issue_v(value_source(1), v1);
+    all_k(key_source(0), k0);
+    all_k(key_source(1), k1);
+    all_v(value_source(0), v0);
+    all_v(value_source(1), v1);
     const uint64_t ksrc = key_source(2), vsrc = value_source(2);
     arrive(std::integral_constant<int, 3 * NI>{});
 #pragma unroll
@@ -290,13 +299,13 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
     rescale(mx);
     arrive(std::integral_constant<int, NI>{});
-    issue_k(ksrc, k0);
-    issue_v(vsrc, v2);
+    all_k(ksrc, k0);
+    all_v(vsrc, v2);
     clear_holes(0, v0);
     read_k(k1, 0, fr[0]);
     const int last = tl.n - 1;
     for (int t = 0; t < last; t += RING) {
-      if (t % (PF_IDS / 2) == 0 && t) load_ids(t + PF_IDS / 2, PF_IDS / 2);
+      if (__builtin_expect(t % (PF_IDS / 2) == 0 && t, 0)) load_ids(t + PF_IDS / 2, PF_IDS / 2);
       iteration(std::integral_constant<int, 0>{}, t, sa, sb);
       if (t + 1 >= last) break;
       iteration(std::integral_constant<int, 1>{}, t + 1, sb, sa);
