@@ -75,14 +75,15 @@ struct AttnTiles {
 template <int TS>
 __device__ __forceinline__ AttnTiles attn_tiles(const AttnArgs& a, int first, int last) {
   AttnTiles t;
-  t.hi = max(last + 1, 0);
-  t.lo = attn_window_lo(a, first);
+  t.hi = uniform(max(last + 1, 0));
+  t.lo = uniform(attn_window_lo(a, first));
   t.sinks = a.window ? a.sinks : 0;
   t.b0 = t.lo / TS;
   t.na = (min(t.sinks, t.hi) + TS - 1) / TS;
   if (t.na >= t.b0) t.na = t.b0 = 0;
-  t.n = t.na + (t.hi + TS - 1) / TS - t.b0;
-  if (t.hi == 0) t.n = 0;
+  t.n = uniform(t.hi ? t.na + (t.hi + TS - 1) / TS - t.b0 : 0);
+  t.na = uniform(t.na);
+  t.b0 = uniform(t.b0);
   return t;
 }
 

@@ -99,7 +99,7 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
     for (int i = tid; i < TS / 16 * n; i += NW * 64) {
       const int v = first_tile + i / (TS / 16), part = i % (TS / 16);
       const int key = min(TS * tl.tile(min(v, tl.n - 1)) + 16 * part, s.len - 1);
-      ids[TS / 16 * (v % PF_IDS) + part] =
+      ids[TS / 16 * (v & (PF_IDS - 1)) + part] =
           min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
     }
     asm volatile("" ::: "memory");
@@ -113,10 +113,12 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   const int lchunk = CPI * w + (TS == 64 ? 0 : half);
   const uint64_t kbase = reinterpret_cast<uint64_t>(a.k) + static_cast<uint64_t>(kvh) * head_bytes +
                          ((lchunk << a.page_shift) + (lkey & (ps - 1))) * 16;
-  auto key_source = [&](int v) __attribute__((always_inline)) {
-    const int vt = min(v, tl.n - 1);
-    const uint32_t id = ids[TS / 16 * (vt % PF_IDS) + (lkey >> 4)];
-    return static_cast<uint64_t>(id) * page_bytes + kbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * 16;
+  auto key_page = [&](int v) __attribute__((always_inline)) {
+    return ids[TS / 16 * (min(v, tl.n - 1) & (PF_IDS - 1)) + (lkey >> 4)];
+  };
+  auto key_source = [&](int v, int id) __attribute__((always_inline)) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes + kbase +
+           static_cast<uint32_t>((TS * tl.tile(min(v, tl.n - 1))) & (ps - 1)) * 16;
   };
   auto issue_k = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
     __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
@@ -126,22 +128,26 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   constexpr int WK = TS / NW;
   const uint64_t vbase = reinterpret_cast<uint64_t>(a.v) + static_cast<uint64_t>(kvh) * head_bytes +
                          ((WK * w) & (ps - 1)) * (2 * D) + lane * 16;
-  auto value_source = [&](int v) __attribute__((always_inline)) {
-    const int vt = min(v, tl.n - 1);
-    const uint32_t id = uniform(ids[TS / 16 * (vt % PF_IDS) + (WK * w >> 4)]);
-    return static_cast<uint64_t>(id) * page_bytes + vbase + static_cast<uint32_t>((TS * tl.tile(vt)) & (ps - 1)) * (2 * D);
+  auto value_page = [&](int v) __attribute__((always_inline)) {
+    return ids[TS / 16 * (min(v, tl.n - 1) & (PF_IDS - 1)) + (WK * w >> 4)];
+  };
+  auto value_source = [&](int v, int id) __attribute__((always_inline)) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes + vbase +
+           static_cast<uint32_t>((TS * tl.tile(min(v, tl.n - 1))) & (ps - 1)) * (2 * D);
   };
   auto issue_v = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
     __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
                                      (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
   };
-  auto all_k = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
+  auto all_k = [&](int v) __attribute__((always_inline)) {
+    const uint64_t p = key_source(v, key_page(v));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) issue_k(p, slot, i);
+    for (int i = 0; i < NI; ++i) issue_k(p, kslot[v % KRING], i);
   };
-  auto all_v = [&](uint64_t p, uint4* slot) __attribute__((always_inline)) {
+  auto all_v = [&](int v) __attribute__((always_inline)) {
+    const uint64_t p = value_source(v, value_page(v));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) issue_v(p, slot, i);
+    for (int i = 0; i < NI; ++i) issue_v(p, vslot[v], i);
   };
   // Waits for this wavefront's transfers but the VM latest, then for the other
   // wavefronts to be here too.
@@ -207,6 +213,7 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       f[j] = __builtin_bit_cast(bf16x8, slot[(2 * (i / DT) + half) * D + 32 * (i % DT) + r]);
     }
   };
+  int kid = 0, vid = 0;          // pages of the keys and values to bring next
   // Pair p of the scores to weights, their sum to l.
   uint32_t pk[2 * SUB][4];
   auto weigh = [&](int p, const f32x16 (&x)[SUB]) __attribute__((always_inline)) {
@@ -231,7 +238,7 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   const int inner1 = uniform(p_first < 0 ? 0 : (p_first + 1) / TS - tl.b0 + tl.na);
   auto iteration = [&](auto jc, int t, f32x16 (&x)[SUB], f32x16 (&y)[SUB]) __attribute__((always_inline)) {
     constexpr int J = decltype(jc)::value;       // t % RING
-    uint64_t ksrc = 0, vsrc = 0;
+    constexpr int GAP = NSB / (2 * NI) < 3 ? NSB / (2 * NI) : 3;   // steps between transfers
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
       const int g = i / 4, sub = i / KS;
@@ -244,8 +251,6 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 #pragma unroll
       for (int j = 0; j < PA; ++j)
         if (i % SA == 0) weigh(i / SA * PA + j, x);
-      if (i == 1) ksrc = key_source(t + 3);
-      if (i == 2) vsrc = value_source(t + 3);
       __builtin_amdgcn_sched_barrier(0);
     }
     arrive(std::integral_constant<int, NI>{});
@@ -254,6 +259,7 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       mask(t + 1, y);
     }
     float mx = y[0][0];
+    uint64_t ksrc = 0, vsrc = 0;
 #pragma unroll
     for (int i = 0; i < NSB; ++i) {
       const int g = i / 4;
@@ -262,8 +268,14 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
         if (g + 1 < NGB) read_v(vslot[J], g + 1, fr[(g + 1) & 1]);
         else read_k(kslot[J % KRING], 0, fr[0]);
       }
-      if (i >= 1 && i <= NI) issue_k(ksrc, kslot[(J + 1) % KRING], i - 1);
-      if (i > NI && i <= 2 * NI) issue_v(vsrc, vslot[(J + 3) % RING], i - NI - 1);
+      if (i == 0) ksrc = key_source(t + 3, kid);
+      if (i == NI * GAP) vsrc = value_source(t + 3, vid);
+      if (i % GAP == GAP - 1 && i / GAP < NI) issue_k(ksrc, kslot[(J + 1) % KRING], i / GAP);
+      if (i % GAP == GAP - 1 && i / GAP >= NI && i / GAP < 2 * NI) issue_v(vsrc, vslot[(J + 3) % RING], i / GAP - NI);
+      if (i == NSB - 1) {
+        kid = key_page(t + 4);
+        vid = value_page(t + 4);
+      }
 #pragma unroll
       for (int j = 0; j < PB; ++j)
         if (i % SB == 0) {
@@ -279,11 +291,12 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   if (tl.n > 0) {
     load_ids(0, PF_IDS);
     __syncthreads();
-    all_k(key_source(0), k0);
-    all_k(key_source(1), k1);
-    all_v(value_source(0), v0);
-    all_v(value_source(1), v1);
-    const uint64_t ksrc = key_source(2), vsrc = value_source(2);
+    all_k(0);
+    all_k(1);
+    all_v(0);
+    all_v(1);
+    kid = key_page(3);
+    vid = value_page(3);
     arrive(std::integral_constant<int, 3 * NI>{});
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
@@ -299,8 +312,8 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
     rescale(mx);
     arrive(std::integral_constant<int, NI>{});
-    all_k(ksrc, k0);
-    all_v(vsrc, v2);
+    all_k(2);
+    all_v(2);
     clear_holes(0, v0);
     read_k(k1, 0, fr[0]);
     const int last = tl.n - 1;
