@@ -100,10 +100,13 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
     const int64_t seen = cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32);
     if (seen < tiles) tiles = seen;
   }
-  const int64_t nw = c->head_dim * p.ct >= 256 ? 4 : 8;
-  // parts of nw tiles, twice as many, ... until one block per CU is left
-  int64_t tps = nw;
-  while (tps < ATTN_MAX_TPS && B * c->n_kv_heads * p.col_blocks * cdiv(tiles, tps) > 1024) tps *= 2;
+  // parts that together fill the places of the GPU's 256 CUs once, if all
+  // sequences were as long as the longest may be; no smaller than a tile per
+  // wavefront, and no larger than ATTN_MAX_TPS, since the others should not
+  // wait for one long sequence
+  const int64_t places = 256 * attn_blocks_per_cu(c->head_dim, p.ct);
+  int64_t tps = cdiv(cdiv(B * c->n_kv_heads * p.col_blocks * tiles, places), ATTN_NW) * ATTN_NW;
+  tps = tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
   p.tiles_per_split = static_cast<int>(tps);
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
   if (p.splits > 1) p.ws_bytes = size_t(B) * c->n_kv_heads * cols * p.splits * (c->head_dim + 2) * 4;
@@ -113,7 +116,7 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
 template <int D, int CT>
 int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
   const int64_t blocks = int64_t(a.B) * a.kv_heads * p.col_blocks * p.splits;
-  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(blocks)), dim3(DecodeShape<D, CT>::NW * 64), s, a);
+  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(blocks)), dim3(ATTN_NW * 64), s, a);
   if (st || p.splits == 1) return st;
   return launch(k_attn_join<D>, dim3(static_cast<unsigned>(int64_t(a.B) * a.n_q * a.heads)), dim3(256), s, a);
 }
