@@ -2,10 +2,20 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * w;  (a, b) -> (a c - b s, b c + a s)
 //
-// A lane holds 8 neighbouring dims (16 bytes) of one head row, D / 8 lanes a
-// row, so the mean square is a reduction over D / 8 lanes and the other half
-// of a rotated pair is in the same lane (neighbouring pairs) or rotary / 16
-// lanes away (halves).  Everything is fp32 between the load and one rounding.
+// What bounds it: the rows are read once and written once, a few operations a
+// value; with one token, the launch.  So:
+//   * a lane holds 8 dims of one row, D / 8 lanes a row, in two pieces of 4: the
+//     two halves of 4 rotated pairs, or 8 neighbouring dims.  Either way the
+//     rotation stays in the lane and takes the table's entries 4 c .. 4 c + 3,
+//     and the mean square is a sum over D / 8 lanes; everything is fp32 between
+//     the load and one rounding;
+//   * a block keeps its 2048 / D tokens and goes through several heads, so that
+//     a token's cosines and sines, as long as two of its rows, are read once
+//     for all of them and the next row is on its way while one is worked on;
+//   * the cache's order of keys (16 bytes of a token, then the next token's) and
+//     of values (8 tokens of a dim) is made in LDS, so that the stores are runs
+//     of a block's tokens.  Eight tokens whose slots are not one aligned run of
+//     8 store their values one by one.
 #pragma once
 
 #include "attn.hpp"
@@ -24,86 +34,141 @@ struct PrepArgs {
   const int64_t* slots;
   int64_t stride, T, n_positions, n_slots;
   int32_t heads, kv_heads, page_shift, rotary, interleaved;
+  int32_t rows_per_block;    // heads that a block goes through
   float eps;
 };
 
 // blockIdx.x: block of 2048 / D tokens (256 threads of 8 dims); blockIdx.y:
-// head row of qkv (query heads, key heads, value heads).
+// rows_per_block rows of qkv (query heads, key heads, value heads).
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
   constexpr int LR = D / 8, TB = 256 / LR;
   const int tid = threadIdx.x, c = tid % LR, tt = tid / LR;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * TB + tt;
-  const int h = blockIdx.y;
-  const bool live = t < a.T;
-  const int64_t tl = live ? t : a.T - 1;
-  const uint4 raw = *reinterpret_cast<const uint4*>(a.qkv + tl * a.stride + static_cast<int64_t>(h) * D + 8 * c);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  const int64_t slot = live && h >= a.heads ? a.slots[t] : -1;
-  const bool store = slot >= 0 && slot < a.n_slots;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TB;
+  const int64_t t = min(t0 + tt, a.T - 1);         // past the end: the last token again, not stored
+  const bool live = t0 + tt < a.T;
+  const int rows = a.heads + 2 * a.kv_heads;
+  const int r0 = blockIdx.y * a.rows_per_block, r1 = min(r0 + a.rows_per_block, rows);
+  // this lane's dims: d0 .. d0 + 3 and d1 .. d1 + 3
+  const int half = a.rotary >> 1;
+  const bool turned = 8 * c < a.rotary;
+  const bool apart = turned && !a.interleaved;
+  const int d0 = apart ? 4 * c : 8 * c, d1 = apart ? half + 4 * c : 8 * c + 4;
+  const uint16_t* const x0 = a.qkv + t * a.stride;
+  uint2 raw0 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d0);
+  uint2 raw1 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d1);
+
+  __shared__ int64_t lslot[TB];
+  __shared__ __align__(16) uint16_t tile[2048];
   const int ps = 1 << a.page_shift;
-  const int64_t page = slot >> a.page_shift;
-  const int at = static_cast<int>(slot & (ps - 1));
-  if (h >= a.heads + a.kv_heads) {
-    if (!store) return;
-    const int64_t o = (page * a.kv_heads + (h - a.heads - a.kv_heads)) * (static_cast<int64_t>(D) << a.page_shift) +
-                      (static_cast<int64_t>(at >> 3) * D + 8 * c) * 8 + (at & 7);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a.v[o + 8 * j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-    return;
+  if (r1 > a.heads) {
+    if (tid < TB) lslot[tid] = t0 + tid < a.T ? a.slots[t0 + tid] : -1;
   }
-  float x[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = bf16_to_f32(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
-  const bool isq = h < a.heads;
-  const float* nw = isq ? a.qw : a.kw;
-  if (nw) {
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-#pragma unroll
-    for (int m = 1; m < LR; m <<= 1) s += __shfl_xor(s, m);
-    const float r = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * nw[8 * c + j];
+  f32x4 co = {1.0f, 1.0f, 1.0f, 1.0f}, si = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (turned && r0 < a.heads + a.kv_heads) {
+    const int64_t pos = min(max(static_cast<int64_t>(a.positions[t]), int64_t(0)), a.n_positions - 1);
+    const float* cs = a.cos_sin + pos * a.rotary + 4 * c;
+    co = *reinterpret_cast<const f32x4*>(cs);
+    si = *reinterpret_cast<const f32x4*>(cs + half);
   }
-  if (a.rotary) {
-    const int64_t pos = min(max(static_cast<int64_t>(a.positions[tl]), int64_t(0)), a.n_positions - 1);
-    const float* cs = a.cos_sin + pos * a.rotary;
-    const int half = a.rotary >> 1;
-    if (a.interleaved) {
-      if (8 * c < a.rotary) {
+  f32x4 n0 = {}, n1 = {};
+  if (r1 > a.heads) __syncthreads();
+
+  for (int h = r0; h < r1; ++h) {
+    const uint2 now0 = raw0, now1 = raw1;
+    if (h + 1 < r1) {
+      raw0 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d0);
+      raw1 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d1);
+    }
+    const bool isq = h < a.heads;
+    if (h >= a.heads + a.kv_heads) {
+      // values: thread (g, d) stores dim d of tokens 8 g .. 8 g + 7
+      __syncthreads();
+      *reinterpret_cast<uint2*>(tile + tt * D + d0) = now0;
+      *reinterpret_cast<uint2*>(tile + tt * D + d1) = now1;
+      __syncthreads();
+      const int d = tid % D, g = tid / D;
+      const uint16_t* col = tile + 8 * g * D + d;
+      uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float co = cs[4 * c + j], si = cs[half + 4 * c + j];
-          const float p = x[2 * j], q = x[2 * j + 1];
-          x[2 * j] = p * co - q * si;
-          x[2 * j + 1] = q * co + p * si;
+      for (int j = 0; j < 4; ++j) w[j] = col[2 * j * D] | static_cast<uint32_t>(col[(2 * j + 1) * D]) << 16;
+      const int64_t s0 = lslot[8 * g];
+      bool run = s0 >= 0 && s0 < a.n_slots && (s0 & 7) == 0;
+#pragma unroll
+      for (int j = 1; j < 8; ++j) run = run && lslot[8 * g + j] == s0 + j;
+      auto place = [&](int64_t slot) {
+        return ((slot >> a.page_shift) * a.kv_heads + (h - a.heads - a.kv_heads)) *
+                   (static_cast<int64_t>(D) << a.page_shift) +
+               (((slot & (ps - 1)) >> 3) * D + d) * 8 + (slot & 7);
+      };
+      if (run) {
+        *reinterpret_cast<uint4*>(a.v + place(s0)) = uint4{w[0], w[1], w[2], w[3]};
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t slot = lslot[8 * g + j];
+          if (slot >= 0 && slot < a.n_slots) a.v[place(slot)] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
         }
       }
-    } else {
-      const int hl = half >> 3;                 // lanes of half a rotation
-      const int lane = tid & 63;
-      const int other = c < hl ? lane + hl : c < 2 * hl ? lane - hl : lane;
-      const int i0 = 8 * (c < hl ? c : c - hl);
-      const float sg = c < hl ? -1.0f : 1.0f;
-      float y[8];
+      continue;
+    }
+    const uint32_t w[4] = {now0.x, now0.y, now1.x, now1.y};
+    float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __shfl(x[j], other);
-      if (c < 2 * hl) {
+    for (int j = 0; j < 8; ++j) x[j] = bf16_to_f32(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+    const float* norm = isq ? a.qw : a.kw;
+    if (norm) {
+      if (h == r0 || h == a.heads) {
+        n0 = *reinterpret_cast<const f32x4*>(norm + d0);
+        n1 = *reinterpret_cast<const f32x4*>(norm + d1);
+      }
+      float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[i0 + j] + sg * y[j] * cs[half + i0 + j];
+      for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+      s = dpp_add<DPP_QUAD_1032>(s);
+      s = dpp_add<DPP_QUAD_2301>(s);
+      s = dpp_add<DPP_ROW_HALF_MIRROR>(s);
+      if (LR > 8) s = dpp_add<DPP_ROW_MIRROR>(s);
+      if (LR > 16) s += __shfl_xor(s, 16);
+      const float r = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = x[j] * r * n0[j];
+        x[4 + j] = x[4 + j] * r * n1[j];
       }
     }
-  }
-  const uint4 res = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                     pack_bf16x2(x[6], x[7])};
-  if (isq) {
-    if (live) *reinterpret_cast<uint4*>(a.q_out + (t * a.heads + h) * D + 8 * c) = res;
-  } else if (store) {
-    const int64_t o = (page * a.kv_heads + (h - a.heads)) * (static_cast<int64_t>(D) << a.page_shift) +
-                      (static_cast<int64_t>(c) * ps + at) * 8;
-    *reinterpret_cast<uint4*>(a.k + o) = res;
+    if (a.rotary) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // pair j: dims (2 j, 2 j + 1) of the lane's 8, or (j, 4 + j)
+        const float p = a.interleaved ? x[2 * j] : x[j], q = a.interleaved ? x[2 * j + 1] : x[4 + j];
+        const float u = p * co[j] - q * si[j], v = q * co[j] + p * si[j];
+        (a.interleaved ? x[2 * j] : x[j]) = u;
+        (a.interleaved ? x[2 * j + 1] : x[4 + j]) = v;
+      }
+    }
+    const uint2 res0 = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    const uint2 res1 = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    if (isq) {
+      if (live) {
+        uint16_t* o = a.q_out + (t * a.heads + h) * D;
+        *reinterpret_cast<uint2*>(o + d0) = res0;
+        *reinterpret_cast<uint2*>(o + d1) = res1;
+      }
+    } else {
+      // keys: thread (chunk, token) stores 16 bytes
+      __syncthreads();
+      *reinterpret_cast<uint2*>(tile + ((d0 >> 3) * TB + tt) * 8 + (d0 & 7)) = res0;
+      *reinterpret_cast<uint2*>(tile + ((d1 >> 3) * TB + tt) * 8 + (d1 & 7)) = res1;
+      __syncthreads();
+      const int ch = tid / TB;
+      const int64_t slot = lslot[tid % TB];
+      if (slot >= 0 && slot < a.n_slots)
+        *reinterpret_cast<uint4*>(a.k + ((slot >> a.page_shift) * a.kv_heads + (h - a.heads)) *
+                                            (static_cast<int64_t>(D) << a.page_shift) +
+                                  ((static_cast<int64_t>(ch) << a.page_shift) + (slot & (ps - 1))) * 8) =
+            *reinterpret_cast<const uint4*>(tile + 8 * tid);
+    }
   }
 }
 

@@ -50,6 +50,8 @@ int validate_cache(const moe_attn_config* c, const moe_attn_cache* cache) {
   return MOE_MLP_OK;
 }
 
+constexpr int64_t PREP_BLOCKS = 1024;              // blocks of moe_attn_prepare that fill the GPU
+
 // hipLaunchKernel says whether this launch failed; an error that an earlier
 // call of the process left behind is not taken for it.
 template <typename A>
@@ -225,8 +227,12 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
   hipStream_t s = static_cast<hipStream_t>(stream);
   return with_dim(cfg->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    return launch(k_attn_prepare<D>, dim3(static_cast<unsigned>(cdiv(T, 2048 / D)), static_cast<unsigned>(rows)),
-                  dim3(256), s, a);
+    const int64_t token_blocks = cdiv(T, 2048 / D);
+    // one head a block while the blocks are few, up to 8 with thousands of them
+    const int64_t per = rows * token_blocks / PREP_BLOCKS;
+    a.rows_per_block = static_cast<int32_t>(per < 1 ? 1 : per > 8 ? 8 : per);
+    return launch(k_attn_prepare<D>, dim3(static_cast<unsigned>(token_blocks),
+                                          static_cast<unsigned>(cdiv(rows, a.rows_per_block))), dim3(256), s, a);
   });
 }
 
