@@ -98,11 +98,12 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
 
 /*
  * Workspace bytes of moe_attn_decode (prefill == 0; max_q = its n_q) or
- * moe_attn_prefill (prefill != 0) for B sequences of at most max_q new tokens
- * and at most max_len tokens in all.  `bytes` is a HOST pointer.
+ * moe_attn_prefill (prefill != 0) for T new tokens (decode: B * n_q) of B
+ * sequences of at most max_q new tokens and at most max_len tokens in all.
+ * `bytes` is a HOST pointer.
  */
-int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t max_q, int64_t max_len, int prefill,
-                            size_t* bytes);
+int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
+                            int prefill, size_t* bytes);
 
 /*
  * Attention of n_q new tokens (1..MOE_ATTN_DECODE_MAX_Q: one, or a verify

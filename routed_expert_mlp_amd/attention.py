@@ -51,7 +51,7 @@ def _lib() -> ctypes.CDLL:
         vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
         cfgp, cp = ctypes.POINTER(moe_attn_config), ctypes.POINTER(moe_attn_cache)
         L.moe_attn_prepare.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp]
-        L.moe_attn_workspace_size.argtypes = [cfgp, i64, i64, i64, ctypes.c_int, ctypes.POINTER(sz)]
+        L.moe_attn_workspace_size.argtypes = [cfgp, i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(sz)]
         L.moe_attn_decode.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         L.moe_attn_prefill.argtypes = [cfgp, cp, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         for n in EXPORTED:
@@ -107,16 +107,18 @@ def new_cache(cfg: AttnConfig, n_pages: int, device="cuda") -> KVCache:
                    torch.empty(v, dtype=torch.bfloat16, device=device))
 
 
-def moe_attn_workspace_size(cfg: AttnConfig, B: int, max_q: int, max_len: int, prefill: bool) -> int:
+def moe_attn_workspace_size(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill: bool) -> int:
+    """Bytes for T new tokens of B sequences, at most max_q of one, each of at most max_len tokens in all."""
     n = ctypes.c_size_t(0)
-    _check(_lib().moe_attn_workspace_size(ctypes.byref(cfg.c()), int(B), int(max_q), int(max_len),
+    _check(_lib().moe_attn_workspace_size(ctypes.byref(cfg.c()), int(T), int(B), int(max_q), int(max_len),
                                           int(bool(prefill)), ctypes.byref(n)), "moe_attn_workspace_size")
     return n.value
 
 
-def workspace(cfg: AttnConfig, B: int, max_q: int, max_len: int, prefill: bool, device="cuda") -> torch.Tensor:
+def workspace(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill: bool,
+              device="cuda") -> torch.Tensor:
     """A workspace tensor of the size the library asks for (allocated by torch)."""
-    return torch.empty(max(1, moe_attn_workspace_size(cfg, B, max_q, max_len, prefill)), dtype=torch.uint8,
+    return torch.empty(max(1, moe_attn_workspace_size(cfg, T, B, max_q, max_len, prefill)), dtype=torch.uint8,
                        device=device)
 
 
@@ -127,13 +129,13 @@ def _one_device(**tensors) -> None:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
 
 
-def _ws_on_stream(cfg, B, max_q, max_len, prefill, device, stream) -> torch.Tensor:
+def _ws_on_stream(cfg, T, B, max_q, max_len, prefill, device, stream) -> torch.Tensor:
     """A workspace that torch's allocator ties to the stream that the call runs on."""
     handle = _stream(stream)
     if handle == torch.cuda.current_stream().cuda_stream:
-        return workspace(cfg, B, max_q, max_len, prefill, device)
+        return workspace(cfg, T, B, max_q, max_len, prefill, device)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
-        return workspace(cfg, B, max_q, max_len, prefill, device)
+        return workspace(cfg, T, B, max_q, max_len, prefill, device)
 
 
 def _callable(name: str, args, keep):
@@ -191,7 +193,7 @@ def bind_decode(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: torc
     _check_tensor(out, "out", tuple(q.shape), torch.bfloat16)
     pages = _check_sequences(cfg, cache, B, seq_lens, page_table)
     if ws is None:
-        ws = _ws_on_stream(cfg, B, n, max_len, False, q.device, stream)
+        ws = _ws_on_stream(cfg, B * n, B, n, max_len, False, q.device, stream)
     _check_tensor(ws, "workspace", None, torch.uint8)
     _one_device(q=q, out=out, k=cache.k, v=cache.v, seq_lens=seq_lens, page_table=page_table, workspace=ws)
     c, cc = cfg.c(), cache.c()
@@ -213,7 +215,7 @@ def bind_prefill(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, cu_q: torch.T
     _check_tensor(cu_q, "cu_q", (B + 1,), torch.int32)
     pages = _check_sequences(cfg, cache, B, seq_lens, page_table)
     if ws is None:
-        ws = _ws_on_stream(cfg, B, max_q, max_len, True, q.device, stream)
+        ws = _ws_on_stream(cfg, T, B, max_q, max_len, True, q.device, stream)
     _check_tensor(ws, "workspace", None, torch.uint8)
     _one_device(q=q, out=out, k=cache.k, v=cache.v, cu_q=cu_q, seq_lens=seq_lens, page_table=page_table,
                 workspace=ws)

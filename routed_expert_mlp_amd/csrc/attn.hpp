@@ -28,7 +28,7 @@ struct AttnArgs {
   int32_t heads, kv_heads, group;
   int32_t page_shift;
   int32_t window, sinks;      // window 0: none
-  int32_t splits, tiles_per_split;   // decode: parts of the visible tiles
+  int32_t splits, tiles_per_split;   // parts of the visible tiles (at most), and their size
   float scale_log2;           // scale * log2(e): the softmax runs on exp2
 };
 
@@ -69,7 +69,19 @@ __device__ __forceinline__ int attn_window_lo(const AttnArgs& a, int p) {
 struct AttnTiles {
   int na, b0, n;
   int lo, hi, sinks;        // visible to some position: key < hi and (key >= lo or key < sinks)
-  __device__ __forceinline__ int tile(int v) const { return v < na ? v : v - na + b0; }
+  int skip;                 // tiles before the part that n counts
+  __device__ __forceinline__ int tile(int v) const {
+    v += skip;
+    return v < na ? v : v - na + b0;
+  }
+  // Keeps part `split` of parts of `size` tiles; false if there is none, except for an empty first one.
+  __device__ __forceinline__ bool keep_part(int split, int size) {
+    skip = split * size;
+    n = min(n - skip, size);
+    if (n > 0) return true;
+    n = 0;
+    return split == 0;
+  }
 };
 
 template <int TS>
@@ -84,6 +96,7 @@ __device__ __forceinline__ AttnTiles attn_tiles(const AttnArgs& a, int first, in
   t.n = uniform(t.hi ? t.na + (t.hi + TS - 1) / TS - t.b0 : 0);
   t.na = uniform(t.na);
   t.b0 = uniform(t.b0);
+  t.skip = 0;
   return t;
 }
 
@@ -137,6 +150,21 @@ __device__ __forceinline__ float sum_halves(float v) {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Rows that are read or written once and not soon again go around the caches
+// (131071 keys: 100 us with ordinary loads, 89 us with these; 4096 tokens
+// prepared: 22.7 us and 21.5 us).
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return uint4{v.x, v.y, v.z, v.w};
+}
+
+__device__ __forceinline__ uint2 load_stream(const uint2* p) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+  return uint2{v.x, v.y};
+}
 
 // Below every score, and finite: the running maximum of a row that has seen nothing.
 constexpr float ATTN_NO_MAX = -1e30f;

@@ -35,15 +35,6 @@ constexpr int ATTN_NW = 4;            // wavefronts of a block
 // operands (at most 256 and 512).
 constexpr int attn_blocks_per_cu(int D, int CT) { return D * CT <= 128 ? 2 : 1; }
 
-// Keys and values are read once and not again before the next token: loaded as
-// a stream, they do not push anything out of the caches (131071 keys: 100 us
-// with ordinary loads, 89 us with these).
-__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  return uint4{v.x, v.y, v.z, v.w};
-}
-
 // Column col of a sequence and key/value head: new token col / group, head col % group.
 __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int kvh, int col) {
   const int t = col / a.group;
@@ -79,18 +70,17 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
   }
   const AttnSeq s = attn_seq(a, b);
   const int first = s.len - s.n;
-  const AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
-  const int v0 = split * a.tiles_per_split, v1 = min(v0 + a.tiles_per_split, tl.n);
-  if (v0 >= v1 && split > 0) return;
+  AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
   const bool whole = tl.n <= a.tiles_per_split;
+  if (!tl.keep_part(split, a.tiles_per_split)) return;
 
   __shared__ int ids[2 * ATTN_MAX_TPS];
   __shared__ float lm[NW][COLS], ll[NW][COLS];
   __shared__ float lo_[NW / 2][COLS * LD];
 
   // page of each 16 keys of this part
-  for (int i = tid; i < 2 * (v1 - v0); i += NW * 64) {
-    const int key = min(32 * tl.tile(v0 + (i >> 1)) + 16 * (i & 1), s.len - 1);
+  for (int i = tid; i < 2 * tl.n; i += NW * 64) {
+    const int key = min(32 * tl.tile(i >> 1) + 16 * (i & 1), s.len - 1);
     ids[i] = min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
   }
 
@@ -102,21 +92,21 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
   const int64_t head_elems = static_cast<int64_t>(D) << a.page_shift;
   auto load_k = [&](int v, uint4 (&kf)[KS]) {
     const int key = 32 * tl.tile(v) + swap23(r);
-    const int64_t base = (static_cast<int64_t>(ids[2 * (v - v0) + (r >> 4)]) * a.kv_heads + kvh) * head_elems +
+    const int64_t base = (static_cast<int64_t>(ids[2 * v + (r >> 4)]) * a.kv_heads + kvh) * head_elems +
                          ((half << a.page_shift) + (key & (ps - 1))) * 8;
     const uint16_t* p = a.k + base;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kf[ks] = load_stream(p + ((2 * ks * 8) << a.page_shift));
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = load_stream(reinterpret_cast<const uint4*>(p + ((2 * ks * 8) << a.page_shift)));
   };
   auto load_v = [&](int v, uint4 (&vf)[2][DT]) {
     const int key0 = 32 * tl.tile(v);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int at = ((key0 + 16 * g) & (ps - 1)) + 8 * half;
-      const uint16_t* p = a.v + (static_cast<int64_t>(ids[2 * (v - v0) + g]) * a.kv_heads + kvh) * head_elems +
+      const uint16_t* p = a.v + (static_cast<int64_t>(ids[2 * v + g]) * a.kv_heads + kvh) * head_elems +
                           at * D + r * 8;
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) vf[g][dt] = load_stream(p + 32 * 8 * dt);
+      for (int dt = 0; dt < DT; ++dt) vf[g][dt] = load_stream(reinterpret_cast<const uint4*>(p + 32 * 8 * dt));
     }
   };
 
@@ -132,12 +122,12 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
       for (int e = 0; e < 16; ++e) acc[ct][dt][e] = 0.0f;
   }
   uint4 kf[KS], vf[2][DT];
-  int v = v0 + w;
-  if (v < v1) {
+  int v = w;
+  if (v < tl.n) {
     load_k(v, kf);
     load_v(v, vf);
   }
-  for (; v < v1; v += NW) {
+  for (; v < tl.n; v += NW) {
     f32x16 sc[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -150,7 +140,7 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
         sc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[ks]), qf[ct][ks], sc[ct], 0, 0,
                                                          0);
     const int vn = v + NW;
-    if (vn < v1) load_k(vn, kf);
+    if (vn < tl.n) load_k(vn, kf);
     const int key0 = 32 * tl.tile(v);
     // a tile that some column sees only in part: scores of invisible keys go to
     // -inf, and the values of keys that nobody sees, whatever the slots hold, to 0
@@ -206,7 +196,7 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
           acc[ct][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g][dt]),
                                                                 __builtin_bit_cast(bf16x8, pf[ct][g]), acc[ct][dt], 0,
                                                                 0, 0);
-    if (vn < v1) load_v(vn, vf);
+    if (vn < tl.n) load_v(vn, vf);
   }
 
   // join the wavefronts: common maximum, then the sums in a tree

@@ -16,6 +16,9 @@
 //     turn those of tile t into weights (phase A), then adds tile t's
 //     weighted values while they look for tile t + 1's maximum (phase B); the
 //     sums are rescaled only when a maximum rises by more than 2^8.
+//   * With few columns and a long cache (a piece of a prompt far into its
+//     sequence) the key tiles are cut into parts, a block each, which
+//     k_attn_prefill_join adds up.
 //   * Fragments are read in groups of four, a group ahead of its use and
 //     across the barrier between the phases.
 #pragma once
@@ -35,6 +38,7 @@ struct PrefillShape {
   static constexpr int TS = D == 256 ? 32 : 64;      // keys of a tile
   static constexpr int NW = D == 128 ? 8 : 4;        // wavefronts of a block
   static constexpr int COLS = 32 * NW;
+  static constexpr int PER_CU = D == 64 ? 2 : 1;     // blocks that a CU holds at once
 };
 
 // Weights may exceed the running maximum by this many powers of two before
@@ -54,9 +58,9 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   // key/value heads run fastest over the blocks: with a multiple of 8 of them
   // the blocks of one stay on one XCD, whose L2 then holds its keys; the
   // longest column blocks start first
-  const int groups = a.B * a.kv_heads;
-  const int gi = blockIdx.x % groups;
-  const int cb = static_cast<int>(gridDim.x) / groups - 1 - static_cast<int>(blockIdx.x) / groups;
+  const int groups = a.B * a.kv_heads, col_blocks = (a.n_q * a.group + COLS - 1) / COLS;
+  const int gi = blockIdx.x % groups, bi = blockIdx.x / groups;
+  const int cb = col_blocks - 1 - bi % col_blocks, split = bi / col_blocks;
   const int kvh = gi % a.kv_heads, b = gi / a.kv_heads;
   const AttnSeq s = attn_seq(a, b);
   const int cols = s.n * a.group;
@@ -66,7 +70,9 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   const int w = uniform(tid >> 6);
   const int first = s.len - s.n;
   const int p_first = uniform(first + c0 / a.group), p_last = uniform(first + (min(c0 + COLS, cols) - 1) / a.group);
-  const AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
+  AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
+  const bool whole = tl.n <= a.tiles_per_split;
+  if (!tl.keep_part(split, a.tiles_per_split)) return;
 
   // slots are arrays of their own, so that the compiler knows which reads a
   // transfer in flight cannot touch
@@ -78,12 +84,13 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 
   // this lane's column
   const int col = min(c0 + 32 * w + r, cols - 1);
-  const int tok = col / a.group;
-  const int pos = first + tok, wlo = attn_window_lo(a, pos);
-  const int64_t row = (s.row0 + tok) * a.heads + kvh * a.group + (col - tok * a.group);
+  auto row_of = [&]() __attribute__((always_inline)) {
+    const int tok = col / a.group;
+    return (s.row0 + tok) * a.heads + kvh * a.group + (col - tok * a.group);
+  };
   bf16x8 qf[KS];
   {
-    const uint16_t* qp = a.q + row * D + 8 * half;
+    const uint16_t* qp = a.q + row_of() * D + 8 * half;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
   }
@@ -169,7 +176,8 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   auto mask = [&](int v, f32x16 (&x)[SUB]) __attribute__((always_inline)) {
     const int key0 = TS * tl.tile(v);
     if (key0 + TS - 1 <= wp_first && (key0 >= wlo_last || key0 + TS <= tl.sinks)) return;
-    const uint64_t see = visible_bits(key0 + 8 * half, pos, wlo, tl.sinks);
+    const int pos = first + col / a.group;
+    const uint64_t see = visible_bits(key0 + 8 * half, pos, attn_window_lo(a, pos), tl.sinks);
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
@@ -234,8 +242,8 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   // t + 3 (past the end the last tile again, which nobody reads); the keys of
   // tile t + 2 and the values of t + 1 have come.
   // tiles inner0 .. inner1 - 1 are visible as a whole to every column
-  const int inner0 = uniform(max(0, (attn_window_lo(a, p_last) + TS - 1) / TS - tl.b0) + tl.na);
-  const int inner1 = uniform(p_first < 0 ? 0 : (p_first + 1) / TS - tl.b0 + tl.na);
+  const int inner0 = uniform(max(0, (attn_window_lo(a, p_last) + TS - 1) / TS - tl.b0) + tl.na - tl.skip);
+  const int inner1 = uniform(p_first < 0 ? 0 : (p_first + 1) / TS - tl.b0 + tl.na - tl.skip);
   auto iteration = [&](auto jc, int t, f32x16 (&x)[SUB], f32x16 (&y)[SUB]) __attribute__((always_inline)) {
     constexpr int J = decltype(jc)::value;       // t % RING
     constexpr int GAP = NSB / (2 * NI) < 3 ? NSB / (2 * NI) : 3;   // steps between transfers
@@ -347,8 +355,21 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   }
 
   const float lt = sum_halves(l);
-  const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
   if (c0 + 32 * w + r >= cols) return;
+  const int64_t row = row_of();
+  if (!whole) {
+    const int64_t item = row * a.splits + split, items = a.T * a.heads * a.splits;
+    if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + 2 * item) = float2{m, lt};
+    float* o = a.ws + item * D + 4 * half;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(o + 32 * dt + 8 * i) =
+            f32x4{acc[dt][4 * i], acc[dt][4 * i + 1], acc[dt][4 * i + 2], acc[dt][4 * i + 3]};
+    return;
+  }
+  const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
   uint16_t* o = a.out + row * D + 4 * half;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
@@ -358,6 +379,51 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
                        pack_bf16x2(acc[dt][4 * i + 2] * inv, acc[dt][4 * i + 3] * inv)};
       *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
     }
+}
+
+// Joins the parts of the columns that k_attn_prefill left in parts: a block
+// takes 16 of a column block's columns, a wavefront four of them in turn,
+// D / 64 dims a lane.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
+  constexpr int TS = PrefillShape<D>::TS, COLS = PrefillShape<D>::COLS, ND = D / 64, PER = COLS / 16;
+  const int groups = a.B * a.kv_heads;
+  const int gi = blockIdx.x % groups, bi = blockIdx.x / groups;
+  const int cb = bi / PER, kvh = gi % a.kv_heads, b = gi / a.kv_heads;
+  const AttnSeq s = attn_seq(a, b);
+  const int cols = s.n * a.group, c0 = cb * COLS, first = s.len - s.n;
+  if (c0 >= cols) return;
+  const AttnTiles tl = attn_tiles<TS>(a, uniform(first + c0 / a.group),
+                                      uniform(first + (min(c0 + COLS, cols) - 1) / a.group));
+  if (tl.n <= a.tiles_per_split) return;
+  const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int64_t items = a.T * a.heads * a.splits;
+  for (int i = 0; i < 4; ++i) {
+    const int col = c0 + 16 * (bi % PER) + 4 * i + w;
+    if (col >= cols) return;
+    const int t = col / a.group;
+    const int64_t row = (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
+    const float2* ml = reinterpret_cast<const float2*>(a.ws + items * D) + row * a.splits;
+    const float* src = a.ws + row * a.splits * D + lane * ND;
+    float M = ATTN_NO_MAX;
+    for (int j = 0; j < parts; ++j) M = fmaxf(M, ml[j].x);
+    float o[ND] = {}, L = 0.0f;
+    for (int j = 0; j < parts; ++j) {
+      const float2 p = ml[j];
+      const float f = exp2_fast(p.x - M);
+      L += p.y * f;
+#pragma unroll
+      for (int n = 0; n < ND; ++n) o[n] += src[static_cast<int64_t>(j) * D + n] * f;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    uint16_t* out = a.out + row * D + lane * ND;
+    if constexpr (ND == 1) out[0] = f32_to_bf16(o[0] * inv);
+    else {
+#pragma unroll
+      for (int n = 0; n < ND; n += 2) *reinterpret_cast<uint32_t*>(out + n) = pack_bf16x2(o[n] * inv, o[n + 1] * inv);
+    }
+  }
 }
 
 }  // namespace moe

@@ -55,8 +55,8 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
   const bool apart = turned && !a.interleaved;
   const int d0 = apart ? 4 * c : 8 * c, d1 = apart ? half + 4 * c : 8 * c + 4;
   const uint16_t* const x0 = a.qkv + t * a.stride;
-  uint2 raw0 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d0);
-  uint2 raw1 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d1);
+  uint2 raw0 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d0));
+  uint2 raw1 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d1));
 
   __shared__ int64_t lslot[TB];
   __shared__ __align__(16) uint16_t tile[2048];
@@ -77,8 +77,8 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
   for (int h = r0; h < r1; ++h) {
     const uint2 now0 = raw0, now1 = raw1;
     if (h + 1 < r1) {
-      raw0 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d0);
-      raw1 = *reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d1);
+      raw0 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d0));
+      raw1 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d1));
     }
     const bool isq = h < a.heads;
     if (h >= a.heads + a.kv_heads) {

@@ -4,8 +4,10 @@
 // state.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/moe_attn.h"
 #include "attn.hpp"
@@ -75,9 +77,10 @@ int with_dim(int head_dim, F&& f) {
 
 // Sizes that both forms of attention check: B sequences, at most max_q new
 // tokens and max_len tokens of each.
-int validate_sizes(const moe_attn_config* c, int64_t B, int64_t max_q, int64_t max_len, int prefill) {
+int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, int prefill) {
   const int st = validate_cfg(c);
   if (st) return st;
+  if (T < 0 || T >= kMaxTokens) return MOE_MLP_ERR_BAD_SHAPE;
   if (B < 0 || max_q < 0 || max_len < 0 || B >= kInt32End || max_q >= kInt32End || max_len >= kInt32End / 2)
     return MOE_MLP_ERR_BAD_SHAPE;
   if (!prefill && (max_q < 1 || max_q > MOE_ATTN_DECODE_MAX_Q)) return MOE_MLP_ERR_BAD_SHAPE;
@@ -115,6 +118,36 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   return p;
 }
 
+// How a prefill call is cut: blocks of columns, and the visible tiles of a
+// block in parts where there are too few blocks to fill the GPU twice over.
+struct PrefillPlan {
+  int64_t col_blocks;
+  int splits, tiles_per_split;
+  size_t ws_bytes;
+};
+
+template <int D>
+PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len) {
+  using S = PrefillShape<D>;
+  PrefillPlan p{};
+  const int64_t group = c->n_heads / c->n_kv_heads;
+  p.col_blocks = cdiv(max_q * group, S::COLS);
+  // column blocks that can have columns: every sequence leaves one unfilled
+  const int64_t busy = std::min(B * p.col_blocks, T * group / S::COLS + B) * c->n_kv_heads;
+  int64_t tiles = cdiv(max_len, S::TS);
+  if (c->window)
+    tiles = std::min(tiles, cdiv(int64_t(c->window) + cdiv(S::COLS, group), S::TS) + 1 + cdiv(c->n_sinks, S::TS));
+  // Two parts for each place of the 256 CUs, if all blocks were as long as the
+  // longest may be (a place left empty at the end costs up to a part); parts
+  // below 16 tiles are not worth their joining.
+  const int64_t places = 256 * S::PER_CU;
+  const int64_t tps = std::max<int64_t>(cdiv(busy * tiles, 2 * places), 16);
+  p.tiles_per_split = static_cast<int>(std::min<int64_t>(tps, kInt32End - 1));
+  p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
+  return p;
+}
+
 template <int D, int CT>
 int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
   const int64_t blocks = int64_t(a.B) * a.kv_heads * p.col_blocks * p.splits;
@@ -127,11 +160,10 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
               int64_t B, int64_t max_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
               int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream, int prefill) {
   size_t need = 0;
-  int st = moe_attn_workspace_size(c, B, max_q, max_len, prefill, &need);
+  int st = moe_attn_workspace_size(c, T, B, max_q, max_len, prefill, &need);
   if (st) return st;
   if (max_pages < 0 || max_pages >= kInt32End || max_len > max_pages * c->page_size) return MOE_MLP_ERR_BAD_SHAPE;
   if (!prefill) T = B * max_q;
-  if (T < 0 || T >= kMaxTokens) return MOE_MLP_ERR_BAD_SHAPE;
   if (B == 0 || T == 0 || max_q == 0) return MOE_MLP_OK;
   st = validate_cache(c, cache);
   if (st) return st;
@@ -177,8 +209,14 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
   }
   return with_dim(c->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    const int64_t blocks = cdiv(max_q * a.group, PrefillShape<D>::COLS) * B * a.kv_heads;
-    return launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks)), dim3(PrefillShape<D>::NW * 64), s, a);
+    using S = PrefillShape<D>;
+    const PrefillPlan p = prefill_plan<D>(c, T, B, max_q, max_len);
+    a.splits = p.splits;
+    a.tiles_per_split = p.tiles_per_split;
+    const int64_t blocks = p.col_blocks * B * a.kv_heads;
+    const int st = launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks * p.splits)), dim3(S::NW * 64), s, a);
+    if (st || p.splits == 1) return st;
+    return launch(k_attn_prefill_join<D>, dim3(static_cast<unsigned>(blocks * (S::COLS / 16))), dim3(256), s, a);
   });
 }
 
@@ -236,13 +274,19 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
   });
 }
 
-int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t max_q, int64_t max_len, int prefill,
-                            size_t* bytes) {
-  const int st = validate_sizes(cfg, B, max_q, max_len, prefill);
+int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
+                            int prefill, size_t* bytes) {
+  const int st = validate_sizes(cfg, T, B, max_q, max_len, prefill);
   if (st) return st;
   if (!bytes) return MOE_MLP_ERR_NULL_ARG;
-  *bytes = prefill ? 0 : decode_plan(cfg, B, max_q, max_len).ws_bytes;
-  return MOE_MLP_OK;
+  if (!prefill) {
+    *bytes = decode_plan(cfg, B, max_q, max_len).ws_bytes;
+    return MOE_MLP_OK;
+  }
+  return with_dim(cfg->head_dim, [&](auto dc) {
+    *bytes = prefill_plan<decltype(dc)::value>(cfg, T, B, max_q, max_len).ws_bytes;
+    return MOE_MLP_OK;
+  });
 }
 
 int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,

@@ -29,9 +29,9 @@ def cache(**kw):
     return A.moe_attn_cache(**base)
 
 
-def size(c, B=2, max_q=1, max_len=64, prefill=0):
+def size(c, B=2, max_q=1, max_len=64, prefill=0, T=4):
     n = ctypes.c_size_t(0)
-    st = A._lib().moe_attn_workspace_size(ctypes.byref(c) if c is not None else None, B, max_q, max_len, prefill,
+    st = A._lib().moe_attn_workspace_size(ctypes.byref(c) if c is not None else None, T, B, max_q, max_len, prefill,
                                           ctypes.byref(n))
     return st, n.value
 
@@ -148,16 +148,25 @@ def test_nothing_to_do_is_ok():
 def test_workspace_size_and_refusal():
     for pf, call in ((0, decode), (1, prefill)):
         assert size(cfg(), prefill=pf, max_len=1 << 62)[0] == capi.ERR_BAD_SHAPE
+        assert size(cfg(), prefill=pf, T=-1)[0] == capi.ERR_BAD_SHAPE
+        assert size(cfg(), prefill=pf, T=1 << 40)[0] == capi.ERR_BAD_SHAPE
         st, need = size(cfg(), B=2, max_q=4, max_len=64, prefill=pf)
         assert st == capi.OK
     # long caches of few rows are split and joined: that needs room
     long = dict(B=1, max_len=131072)
-    st, need = size(cfg(), max_q=1, prefill=0, **long)
-    assert st == capi.OK
-    if need:
-        assert decode(cfg(), cache(), max_pages=8192, wsb=need - 1, **long) == capi.ERR_WORKSPACE_TOO_SMALL
-        assert decode(cfg(), cache(), max_pages=8192, ws=None, wsb=0, **long) == capi.ERR_NULL_ARG
+    st, need = size(cfg(), max_q=1, prefill=0, T=1, **long)
+    assert st == capi.OK and need > 0
+    assert decode(cfg(), cache(), max_pages=8192, wsb=need - 1, **long) == capi.ERR_WORKSPACE_TOO_SMALL
+    assert decode(cfg(), cache(), max_pages=8192, ws=None, wsb=0, **long) == capi.ERR_NULL_ARG
+    st, need = size(cfg(), max_q=100, prefill=1, T=100, **long)
+    assert st == capi.OK and need > 0
+    pre = dict(T=100, max_q=100, max_pages=8192, **long)
+    assert prefill(cfg(), cache(), wsb=need - 1, **pre) == capi.ERR_WORKSPACE_TOO_SMALL
+    assert prefill(cfg(), cache(), ws=None, wsb=0, **pre) == capi.ERR_NULL_ARG
+    # short prompts are not, nor are long ones of many heads
+    assert size(cfg(), B=1, max_q=512, max_len=512, T=512, prefill=1) == (capi.OK, 0)
+    assert size(cfg(n_heads=32, n_kv_heads=8), B=1, max_q=4096, max_len=4096, T=4096, prefill=1) == (capi.OK, 0)
     n = ctypes.c_size_t(0)
     c = cfg()
-    assert A._lib().moe_attn_workspace_size(ctypes.byref(c), 1, 1, 16, 0, None) == capi.ERR_NULL_ARG
+    assert A._lib().moe_attn_workspace_size(ctypes.byref(c), 1, 1, 1, 16, 0, None) == capi.ERR_NULL_ARG
     assert n.value == 0

@@ -172,6 +172,12 @@ PREFILL = [
     (2, 1, 128, 64, [700], [1500], 256, 3),
     (2, 2, 128, 16, [1000], [1000], 0, 0),
     (3, 1, 64, 16, [513], [2000], 0, 0),
+    # few rows far into long sequences: the keys are taken in parts and joined
+    (8, 2, 128, 16, [5, 3, 0, 2], [3000, 40, 0, 1200], 0, 0),
+    (4, 2, 128, 16, [40], [4000], 2500, 700),
+    (6, 2, 256, 64, [33, 1], [1500, 2047], 0, 0),
+    (10, 2, 64, 32, [70], [5001], 0, 0),
+    (4, 1, 128, 128, [9], [4097], 1100, 1),
 ]
 
 
