@@ -382,11 +382,11 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 }
 
 // Joins the parts of the columns that k_attn_prefill left in parts: a block
-// takes 16 of a column block's columns, a wavefront four of them in turn,
-// D / 64 dims a lane.
+// takes 16 of a column block's columns, a wavefront four of them side by side,
+// D / 64 dims a lane, in one pass over the parts with a running maximum.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
-  constexpr int TS = PrefillShape<D>::TS, COLS = PrefillShape<D>::COLS, ND = D / 64, PER = COLS / 16;
+  constexpr int TS = PrefillShape<D>::TS, COLS = PrefillShape<D>::COLS, ND = D / 64, PER = COLS / 16, NC = 4;
   const int groups = a.B * a.kv_heads;
   const int gi = blockIdx.x % groups, bi = blockIdx.x / groups;
   const int cb = bi / PER, kvh = gi % a.kv_heads, b = gi / a.kv_heads;
@@ -398,30 +398,45 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   if (tl.n <= a.tiles_per_split) return;
   const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-  const int64_t items = a.T * a.heads * a.splits;
-  for (int i = 0; i < 4; ++i) {
-    const int col = c0 + 16 * (bi % PER) + 4 * i + w;
-    if (col >= cols) return;
-    const int t = col / a.group;
-    const int64_t row = (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
-    const float2* ml = reinterpret_cast<const float2*>(a.ws + items * D) + row * a.splits;
-    const float* src = a.ws + row * a.splits * D + lane * ND;
-    float M = ATTN_NO_MAX;
-    for (int j = 0; j < parts; ++j) M = fmaxf(M, ml[j].x);
-    float o[ND] = {}, L = 0.0f;
-    for (int j = 0; j < parts; ++j) {
-      const float2 p = ml[j];
-      const float f = exp2_fast(p.x - M);
-      L += p.y * f;
+  const float2* const ml = reinterpret_cast<const float2*>(a.ws + a.T * a.heads * a.splits * D);
+  const int col0 = c0 + 16 * (bi % PER) + NC * w;
+  int64_t row[NC];
+  float M[NC], L[NC], o[NC][ND];
 #pragma unroll
-      for (int n = 0; n < ND; ++n) o[n] += src[static_cast<int64_t>(j) * D + n] * f;
+  for (int i = 0; i < NC; ++i) {
+    const int col = min(col0 + i, cols - 1), t = col / a.group;
+    row[i] = (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
+    M[i] = ATTN_NO_MAX;
+    L[i] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < ND; ++n) o[i][n] = 0.0f;
+  }
+#pragma unroll 4
+  for (int j = 0; j < parts; ++j) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t item = row[i] * a.splits + j;
+      const float2 p = ml[item];
+      const float* src = a.ws + item * D + lane * ND;
+      const float mn = fmaxf(M[i], p.x);
+      const float f = exp2_fast(M[i] - mn), g = exp2_fast(p.x - mn);
+      M[i] = mn;
+      L[i] = L[i] * f + p.y * g;
+#pragma unroll
+      for (int n = 0; n < ND; ++n) o[i][n] = o[i][n] * f + src[n] * g;
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    uint16_t* out = a.out + row * D + lane * ND;
-    if constexpr (ND == 1) out[0] = f32_to_bf16(o[0] * inv);
-    else {
+  }
 #pragma unroll
-      for (int n = 0; n < ND; n += 2) *reinterpret_cast<uint32_t*>(out + n) = pack_bf16x2(o[n] * inv, o[n + 1] * inv);
+  for (int i = 0; i < NC; ++i) {
+    if (col0 + i >= cols) return;
+    const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
+    uint16_t* out = a.out + row[i] * D + lane * ND;
+    if constexpr (ND == 1) {
+      out[0] = f32_to_bf16(o[i][0] * inv);
+    } else {
+#pragma unroll
+      for (int n = 0; n < ND; n += 2)
+        *reinterpret_cast<uint32_t*>(out + n) = pack_bf16x2(o[i][n] * inv, o[i][n + 1] * inv);
     }
   }
 }
