@@ -41,6 +41,44 @@ struct PrefillShape {
   static constexpr int PER_CU = D == 64 ? 2 : 1;     // blocks that a CU holds at once
 };
 
+// Column block r of all sequences' column blocks in a row: its sequence and its
+// number there, counted from the last one (the longest); false past the end.
+// Every wavefront looks it up for itself, 64 sequences at a time.  (With a grid
+// of sequences x the most column blocks instead, most blocks of a ragged batch
+// are empty, and the busy ones fall to the same shader engines: 8 pieces behind
+// prefixes 105 us that way.)
+template <int COLS>
+__device__ __forceinline__ bool prefill_block(const AttnArgs& a, int r, int& b, int& cb) {
+  if (a.B == 1) {
+    b = 0;
+    cb = (attn_seq(a, 0).n * a.group + COLS - 1) / COLS - 1 - r;
+    return cb >= 0;
+  }
+  const int lane = threadIdx.x & 63, T = static_cast<int>(a.T);
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    int n = 0;
+    if (b0 + lane < a.B) {
+      const int r0 = min(max(a.cu_q[b0 + lane], 0), T), r1 = min(max(a.cu_q[b0 + lane + 1], r0), T);
+      n = (min(r1 - r0, a.n_q) * a.group + COLS - 1) / COLS;
+    }
+    int sum = n;                       // column blocks up to and with this lane's sequence
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const int y = __shfl_up(sum, x);
+      sum += lane >= x ? y : 0;
+    }
+    const uint64_t past = __ballot(sum > r);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      b = b0 + l;
+      cb = __builtin_amdgcn_readlane(sum, l) - 1 - r;
+      return true;
+    }
+    r -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
 // Weights may exceed the running maximum by this many powers of two before
 // the sums are rescaled (fp32 sums and bf16 weights have the range).
 constexpr float PF_SLACK = 8.0f;
@@ -56,16 +94,13 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
   constexpr int PA = NP > NSA ? NP / NSA : 1, SA = NP > NSA ? 1 : NSA / NP;   // pairs a step, steps a pair
   constexpr int PB = NP > NSB ? NP / NSB : 1, SB = NP > NSB ? 1 : NSB / NP;
   // key/value heads run fastest over the blocks: with a multiple of 8 of them
-  // the blocks of one stay on one XCD, whose L2 then holds its keys; the
-  // longest column blocks start first
-  const int groups = a.B * a.kv_heads, col_blocks = (a.n_q * a.group + COLS - 1) / COLS;
-  const int gi = blockIdx.x % groups, bi = blockIdx.x / groups;
-  const int cb = col_blocks - 1 - bi % col_blocks, split = bi / col_blocks;
-  const int kvh = gi % a.kv_heads, b = gi / a.kv_heads;
+  // the blocks of one stay on one XCD, whose L2 then holds its keys
+  const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads, split = bi / a.col_blocks;
+  int b, cb;
+  if (!prefill_block<COLS>(a, bi - split * a.col_blocks, b, cb)) return;
   const AttnSeq s = attn_seq(a, b);
   const int cols = s.n * a.group;
   const int c0 = cb * COLS;
-  if (c0 >= cols) return;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
   const int w = uniform(tid >> 6);
   const int first = s.len - s.n;
@@ -387,12 +422,11 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   constexpr int TS = PrefillShape<D>::TS, COLS = PrefillShape<D>::COLS, ND = D / 64, PER = COLS / 16, NC = 4;
-  const int groups = a.B * a.kv_heads;
-  const int gi = blockIdx.x % groups, bi = blockIdx.x / groups;
-  const int cb = bi / PER, kvh = gi % a.kv_heads, b = gi / a.kv_heads;
+  const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads;
+  int b, cb;
+  if (!prefill_block<COLS>(a, bi / PER, b, cb)) return;
   const AttnSeq s = attn_seq(a, b);
   const int cols = s.n * a.group, c0 = cb * COLS, first = s.len - s.n;
-  if (c0 >= cols) return;
   const AttnTiles tl = attn_tiles<TS>(a, uniform(first + c0 / a.group),
                                       uniform(first + (min(c0 + COLS, cols) - 1) / a.group));
   if (tl.n <= a.tiles_per_split) return;

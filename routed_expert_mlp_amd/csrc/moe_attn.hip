@@ -118,7 +118,7 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   return p;
 }
 
-// How a prefill call is cut: blocks of columns, and the visible tiles of a
+// How a prefill call is cut: column blocks of all sequences, and the visible tiles of a
 // block in parts where there are too few blocks to fill the GPU.
 struct PrefillPlan {
   int64_t col_blocks;
@@ -131,9 +131,9 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   using S = PrefillShape<D>;
   PrefillPlan p{};
   const int64_t group = c->n_heads / c->n_kv_heads;
-  p.col_blocks = cdiv(max_q * group, S::COLS);
-  // column blocks that can have columns: every sequence leaves one unfilled
-  const int64_t busy = std::min(B * p.col_blocks, T * group / S::COLS + B) * c->n_kv_heads;
+  // every sequence leaves at most one column block unfilled
+  p.col_blocks = std::min(B * cdiv(max_q * group, S::COLS), T * group / S::COLS + B);
+  const int64_t busy = p.col_blocks * c->n_kv_heads;
   int64_t tiles = cdiv(max_len, S::TS);
   if (c->window)
     tiles = std::min(tiles, cdiv(int64_t(c->window) + cdiv(S::COLS, group), S::TS) + 1 + cdiv(c->n_sinks, S::TS));
@@ -215,7 +215,8 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
     const PrefillPlan p = prefill_plan<D>(c, T, B, max_q, max_len);
     a.splits = p.splits;
     a.tiles_per_split = p.tiles_per_split;
-    const int64_t blocks = p.col_blocks * B * a.kv_heads;
+    a.col_blocks = static_cast<int32_t>(p.col_blocks);
+    const int64_t blocks = p.col_blocks * a.kv_heads;
     const int st = launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks * p.splits)), dim3(S::NW * 64), s, a);
     if (st || p.splits == 1) return st;
     return launch(k_attn_prefill_join<D>, dim3(static_cast<unsigned>(blocks * (S::COLS / 16))), dim3(256), s, a);
