@@ -190,6 +190,18 @@ def test_prefill(heads, kv, dim, page, new, lens, window, sinks):
     check(b, run_prefill(b, pad=2), what)
 
 
+@pytest.mark.parametrize("B", [65, 200])
+def test_prefill_many_sequences(B):
+    """More sequences than a wavefront has lanes, some without new tokens."""
+    rng = np.random.default_rng(B)
+    new = [int(n) for n in rng.integers(0, 9, B)]
+    new[3], new[-1], new[63] = 40, 0, 0
+    lens = [m + int(p) for m, p in zip(new, rng.integers(0, 30, B))]
+    b = make_batch(config(4, 2, 64, 16), lens, new, seed=B)
+    print(f"[case] prefill of {B} sequences", flush=True)
+    check(b, run_prefill(b, pad=1), f"prefill of {B} sequences")
+
+
 def test_prefill_bounds_above_and_equal_scores():
     cfg = config(8, 2, 128, 16)
     b = make_batch(cfg, [40, 96], [40, 20], seed=9, poison=False, q_std=0.0, v_mean=2.0)
