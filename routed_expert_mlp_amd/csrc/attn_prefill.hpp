@@ -33,12 +33,12 @@ constexpr int PF_RING = 4;           // slots for values
 constexpr int PF_KRING = 2;          // slots for keys
 constexpr int PF_IDS = 64;           // tiles whose page ids are in LDS, in two halves
 
-template <int D>
+template <int D, int NW_>
 struct PrefillShape {
-  static constexpr int TS = D == 256 ? 32 : 64;      // keys of a tile
-  static constexpr int NW = D == 128 ? 8 : 4;        // wavefronts of a block
+  static constexpr int NW = NW_;                                          // wavefronts of a block
+  static constexpr int TS = D == 256 || (D == 128 && NW == 4) ? 32 : 64;  // keys of a tile
   static constexpr int COLS = 32 * NW;
-  static constexpr int PER_CU = D == 64 ? 2 : 1;     // blocks that a CU holds at once
+  static constexpr int PER_CU = D == 256 || NW == 8 ? 1 : 2;              // blocks that a CU holds at once
 };
 
 // Column block r of all sequences' column blocks in a row: its sequence and its
@@ -83,9 +83,9 @@ __device__ __forceinline__ bool prefill_block(const AttnArgs& a, int r, int& b, 
 // the sums are rescaled (fp32 sums and bf16 weights have the range).
 constexpr float PF_SLACK = 8.0f;
 
-template <int D>
-__global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
-  constexpr int TS = PrefillShape<D>::TS, NW = PrefillShape<D>::NW, COLS = PrefillShape<D>::COLS;
+template <int D, int NW>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
+  constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS;
   constexpr int RING = PF_RING, KRING = PF_KRING, KS = D / 16, DT = D / 32, SUB = TS / 32;
   constexpr int NGA = SUB * KS / 4, NGB = 2 * SUB * DT / 4;      // groups of 4 matrix instructions of the two phases
   static_assert(NGA % 2 == 0 && NGB % 2 == 0, "fragment buffers alternate");
@@ -335,12 +335,13 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
     load_ids(0, PF_IDS);
     __syncthreads();
     all_k(0);
-    all_k(1);
+    if (tl.n > 1) all_k(1);
     all_v(0);
-    all_v(1);
+    if (tl.n > 1) all_v(1);
     kid = key_page(3);
     vid = value_page(3);
-    arrive(std::integral_constant<int, 3 * NI>{});
+    if (tl.n > 1) arrive(std::integral_constant<int, 3 * NI>{});
+    else arrive(std::integral_constant<int, NI>{});
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
       f32x16 z = {};
@@ -354,9 +355,12 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
     rescale(mx);
-    arrive(std::integral_constant<int, NI>{});
-    all_k(2);
-    all_v(2);
+    if (tl.n > 1) arrive(std::integral_constant<int, NI>{});
+    else arrive(std::integral_constant<int, 0>{});
+    if (tl.n > 1) {
+      all_k(2);
+      all_v(2);
+    }
     clear_holes(0, v0);
     read_k(k1, 0, fr[0]);
     const int last = tl.n - 1;
@@ -419,9 +423,9 @@ __global__ __launch_bounds__(PrefillShape<D>::NW * 64, D == 256 ? 1 : 2) void k_
 // Joins the parts of the columns that k_attn_prefill left in parts: a block
 // takes 16 of a column block's columns, a wavefront four of them side by side,
 // D / 64 dims a lane, in one pass over the parts with a running maximum.
-template <int D>
+template <int D, int NW>
 __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
-  constexpr int TS = PrefillShape<D>::TS, COLS = PrefillShape<D>::COLS, ND = D / 64, PER = COLS / 16, NC = 4;
+  constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS, ND = D / 64, PER = COLS / 16, NC = 4;
   const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads;
   int b, cb;
   if (!prefill_block<COLS>(a, bi / PER, b, cb)) return;

@@ -126,9 +126,9 @@ struct PrefillPlan {
   size_t ws_bytes;
 };
 
-template <int D>
+template <int D, int NW>
 PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len) {
-  using S = PrefillShape<D>;
+  using S = PrefillShape<D, NW>;
   PrefillPlan p{};
   const int64_t group = c->n_heads / c->n_kv_heads;
   // every sequence leaves at most one column block unfilled
@@ -148,6 +148,26 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
   if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
   return p;
+}
+
+// Calls f(head_dim, wavefronts of a block) with both as integral constants.  At
+// 128 dims 8 wavefronts share a tile's transfers (4096 tokens: 135 us, and 149
+// us with 4), but while blocks of 4 do not fill the 256 CUs they are the faster
+// ones, each tile taking them half as long (512 tokens of 16/2 heads behind 4096
+// cached: 36 us, and 41 us with 8), unless the parts are long all the same (512
+// tokens of 32/8 heads behind 65024: 612 us, and 530 us with 8).  Other widths
+// have one form.
+template <typename F>
+int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
+  using four = std::integral_constant<int, 4>;
+  using eight = std::integral_constant<int, 8>;
+  return with_dim(c->head_dim, [&](auto dc) {
+    if constexpr (decltype(dc)::value == 128) {
+      const PrefillPlan p = prefill_plan<128, 4>(c, T, B, max_q, max_len);
+      if (p.col_blocks * c->n_kv_heads > 256 || p.tiles_per_split > 128) return f(dc, eight{});
+    }
+    return f(dc, four{});
+  });
 }
 
 template <int D, int CT>
@@ -209,17 +229,16 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
       return decode<D, 1>(a, p, s);
     });
   }
-  return with_dim(c->head_dim, [&](auto dc) {
-    constexpr int D = decltype(dc)::value;
-    using S = PrefillShape<D>;
-    const PrefillPlan p = prefill_plan<D>(c, T, B, max_q, max_len);
+  return with_prefill_shape(c, T, B, max_q, max_len, [&](auto dc, auto nc) {
+    constexpr int D = decltype(dc)::value, NW = decltype(nc)::value;
+    const PrefillPlan p = prefill_plan<D, NW>(c, T, B, max_q, max_len);
     a.splits = p.splits;
     a.tiles_per_split = p.tiles_per_split;
     a.col_blocks = static_cast<int32_t>(p.col_blocks);
     const int64_t blocks = p.col_blocks * a.kv_heads;
-    const int st = launch(k_attn_prefill<D>, dim3(static_cast<unsigned>(blocks * p.splits)), dim3(S::NW * 64), s, a);
+    const int st = launch(k_attn_prefill<D, NW>, dim3(static_cast<unsigned>(blocks * p.splits)), dim3(NW * 64), s, a);
     if (st || p.splits == 1) return st;
-    return launch(k_attn_prefill_join<D>, dim3(static_cast<unsigned>(blocks * (S::COLS / 16))), dim3(256), s, a);
+    return launch(k_attn_prefill_join<D, NW>, dim3(static_cast<unsigned>(blocks * (2 * NW))), dim3(256), s, a);
   });
 }
 
@@ -286,8 +305,8 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, in
     *bytes = decode_plan(cfg, B, max_q, max_len).ws_bytes;
     return MOE_MLP_OK;
   }
-  return with_dim(cfg->head_dim, [&](auto dc) {
-    *bytes = prefill_plan<decltype(dc)::value>(cfg, T, B, max_q, max_len).ws_bytes;
+  return with_prefill_shape(cfg, T, B, max_q, max_len, [&](auto dc, auto nc) {
+    *bytes = prefill_plan<decltype(dc)::value, decltype(nc)::value>(cfg, T, B, max_q, max_len).ws_bytes;
     return MOE_MLP_OK;
   });
 }
