@@ -121,7 +121,7 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
 // How a prefill call is cut: column blocks of all sequences, and the visible tiles of a
 // block in parts where there are too few blocks to fill the GPU.
 struct PrefillPlan {
-  int64_t col_blocks;
+  int64_t col_blocks, tiles;         // tiles: the most that a column block can see
   int splits, tiles_per_split;
   size_t ws_bytes;
 };
@@ -144,6 +144,7 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   // behind prefixes, 456 blocks for 512 places: 121 us in parts, 105 us whole.
   const int64_t places = 256 * S::PER_CU;
   const int64_t tps = 2 * busy > places ? tiles : std::max<int64_t>(cdiv(busy * tiles, places), 16);
+  p.tiles = tiles;
   p.tiles_per_split = static_cast<int>(std::max<int64_t>(tps, 1));
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
   if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
@@ -151,12 +152,14 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
 }
 
 // Calls f(head_dim, wavefronts of a block) with both as integral constants.  At
-// 128 dims 8 wavefronts share a tile's transfers (4096 tokens: 135 us, and 149
-// us with 4), but while blocks of 4 do not fill the 256 CUs they are the faster
-// ones, each tile taking them half as long (512 tokens of 16/2 heads behind 4096
-// cached: 36 us, and 41 us with 8), unless the parts are long all the same (512
-// tokens of 32/8 heads behind 65024: 612 us, and 530 us with 8).  Other widths
-// have one form.
+// 128 dims a block has 8 wavefronts, which share a tile's transfers, or 4 with
+// tiles of 32 keys, two blocks a CU, of which one starts or ends while the other
+// computes.  Long blocks want the former (32/8 heads: 4096 tokens 133 us, and
+// 149 us with 4; a window of 4096 on 8192 tokens 403 and 419 us), short ones the
+// latter (2048 tokens 53 us, and 59 us with 8; a window of 1024 on 8192 tokens 169
+// and 179 us), and so do those that leave CUs empty (512 tokens of 16/2 heads
+// behind 4096: 36 and 41 us) unless their parts are long all the same (512
+// tokens of 32/8 heads behind 65024: 612 and 530 us).  Other widths have one form.
 template <typename F>
 int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
   using four = std::integral_constant<int, 4>;
@@ -164,7 +167,7 @@ int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t m
   return with_dim(c->head_dim, [&](auto dc) {
     if constexpr (decltype(dc)::value == 128) {
       const PrefillPlan p = prefill_plan<128, 4>(c, T, B, max_q, max_len);
-      if (p.col_blocks * c->n_kv_heads > 256 || p.tiles_per_split > 128) return f(dc, eight{});
+      if (p.tiles > 64 && (p.col_blocks * c->n_kv_heads > 256 || p.tiles_per_split > 128)) return f(dc, eight{});
     }
     return f(dc, four{});
   });
