@@ -33,8 +33,8 @@
  * page ids and positions out of range are clamped into it, tokens with a slot
  * out of range are not stored, and lengths are clamped, so that no access
  * leaves the caller's buffers; the results for such rows are unspecified.
- * Slots of the cache that no visible key occupies are never used, whatever
- * they hold (NaN too), and page ids without a visible key are never followed.
+ * What slots hold that no visible key occupies (NaN too), and the page ids of
+ * pages without a visible key, do not matter.
  */
 #ifndef MOE_ATTN_H
 #define MOE_ATTN_H
