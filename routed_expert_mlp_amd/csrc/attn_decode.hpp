@@ -286,53 +286,54 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
 }
 
 // Joins the parts of one output row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-// Four wavefronts take every fourth part, D / 64 dims a lane.
+// Lane i of every wavefront has part i's maximum and sum (64 parts at a time),
+// so that M and the factors are known after one load; then the four wavefronts
+// add up every fourth part, D / 64 dims a lane, with several loads in flight.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int ND = D / 64;
+  constexpr int ND = D / 64, UNROLL = 4;
   const int cols = a.n_q * a.group;
   const int col = blockIdx.x % cols, kvh = (blockIdx.x / cols) % a.kv_heads, b = blockIdx.x / cols / a.kv_heads;
   const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
   const float2* ml = reinterpret_cast<const float2*>(a.ws + items * D) + item;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  // every lane its part's maximum, and every wavefront its first sums, whether
-  // or not the sequence turns out to have that part
-  const float m0 = ml[min(lane, a.splits - 1)].x;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const float* const sums = a.ws + item * D + lane * ND;
-  float o0[ND];
-#pragma unroll
-  for (int n = 0; n < ND; ++n) o0[n] = sums[static_cast<int64_t>(min(w, a.splits - 1)) * D + n];
+  // asked for before the sequence's length is known: whether it has that part or not
+  const float2 first_ml = ml[min(lane, a.splits - 1)];
   const AttnSeq s = attn_seq(a, b);
   const AttnTiles tl = attn_tiles<32>(a, s.len - s.n, s.len - 1);
   if (tl.n <= a.tiles_per_split) return;
   const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
-  float M = lane < parts ? m0 : ATTN_NO_MAX;
-  for (int i = lane + 64; i < parts; i += 64) M = fmaxf(M, ml[i].x);
+  float M = ATTN_NO_MAX, L = 0.0f, o[ND] = {};
+  for (int p0 = 0; p0 < parts; p0 += 64) {
+    const int here = min(parts - p0, 64);
+    const float2 p = p0 ? ml[p0 + min(lane, here - 1)] : first_ml;
+    const float m = lane < here ? p.x : ATTN_NO_MAX;
+    float mn = fmaxf(M, m);
 #pragma unroll
-  for (int x = 32; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
-  float o[ND] = {}, L = 0.0f;
-  if (w < parts) {
-    const float2 p = ml[w];
-    const float f = exp2_fast(p.x - M);
-    L = p.y * f;
+    for (int x = 32; x; x >>= 1) mn = fmaxf(mn, __shfl_xor(mn, x));
+    const float f = lane < here ? exp2_fast(m - mn) : 0.0f, old = exp2_fast(M - mn);
+    M = mn;
+    L = L * old + wave_sum(lane < here ? p.y * f : 0.0f);
 #pragma unroll
-    for (int n = 0; n < ND; ++n) o[n] = o0[n] * f;
+    for (int n = 0; n < ND; ++n) o[n] *= old;
+    for (int i0 = w; i0 < here; i0 += 4 * UNROLL) {
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int i = min(i0 + 4 * u, here - 1);
+        const float g = i0 + 4 * u < here ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i)) : 0.0f;
+        const float* src = sums + static_cast<int64_t>(p0 + i) * D;
+#pragma unroll
+        for (int n = 0; n < ND; ++n) o[n] += src[n] * g;
+      }
+    }
   }
-  for (int i = w + 4; i < parts; i += 4) {
-    const float2 p = ml[i];
-    const float f = exp2_fast(p.x - M);
-    L += p.y * f;
-#pragma unroll
-    for (int n = 0; n < ND; ++n) o[n] += sums[static_cast<int64_t>(i) * D + n] * f;
-  }
-  __shared__ float lo_[4][D], ll[4];
+  __shared__ float lo_[4][D];
 #pragma unroll
   for (int n = 0; n < ND; ++n) lo_[w][lane * ND + n] = o[n];
-  if (lane == 0) ll[w] = L;
   __syncthreads();
-  const float t = (ll[0] + ll[1]) + (ll[2] + ll[3]);
-  const float inv = t > 0.0f ? 1.0f / t : 0.0f;
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   uint16_t* out = a.out + attn_row(a, s.row0, kvh, col) * D;
   for (int d = threadIdx.x; d < D; d += 256)
     out[d] = f32_to_bf16(((lo_[0][d] + lo_[1][d]) + (lo_[2][d] + lo_[3][d])) * inv);
