@@ -34,7 +34,9 @@
  * out of range are not stored, and lengths are clamped, so that no access
  * leaves the caller's buffers; the results for such rows are unspecified.
  * What slots hold that no visible key occupies (NaN too), and the page ids of
- * pages without a visible key, do not matter.
+ * pages without a visible key, do not matter.  A value that one query of a
+ * sequence sees should be finite for the others too: those that do not see it
+ * give it the weight 0, and 0 * inf is NaN.
  */
 #ifndef MOE_ATTN_H
 #define MOE_ATTN_H
@@ -100,7 +102,9 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
  * Workspace bytes of moe_attn_decode (prefill == 0; max_q = its n_q) or
  * moe_attn_prefill (prefill != 0) for T new tokens (decode: B * n_q) of B
  * sequences of at most max_q new tokens and at most max_len tokens in all.
- * `bytes` is a HOST pointer.
+ * `bytes` is a HOST pointer.  MOE_MLP_ERR_BAD_SHAPE also for sizes whose launch
+ * would have 2^32 threads or more (tens of thousands of sequences that may all
+ * be very long).
  */
 int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
                             int prefill, size_t* bytes);
@@ -113,7 +117,8 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, in
  * (all k <= p when window is 0):
  *   out = sum_k softmax_k(scale q . k) v_k          over the visible keys
  * in fp32, the softmax weights rounded to bf16 before the sum over v, one
- * rounding of the result.  A query that sees no key (n == 0, p < 0) gives 0.
+ * rounding of the result.  Scores (scale q . k) up to 2^28 in magnitude.  A
+ * query that sees no key (n == 0, p < 0) gives 0.
  *   q         [B, n_q, n_heads, head_dim] bf16;  out the same shape.
  *   seq_lens  [B] int32, the new tokens included, at most max_len.
  *   page_table [B, max_pages] int32.
@@ -125,9 +130,10 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
                     int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
- * The same for prompts, or pieces of prompts behind a cached prefix: sequence
- * b has the new tokens cu_q[b] .. cu_q[b+1]-1 of q, the last ones of its
- * seq_lens[b] tokens, all of them in the cache already.
+ * The same (here the weights' sum is that of the rounded ones) for prompts, or
+ * pieces of prompts behind a cached prefix: sequence b has the new tokens
+ * cu_q[b] .. cu_q[b+1]-1 of q, the last ones of its seq_lens[b] tokens, all of
+ * them in the cache already.
  *   q         [T, n_heads, head_dim] bf16;  out the same shape (rows outside
  *             cu_q[0] .. cu_q[B] are not written).
  *   cu_q      [B + 1] int32, not decreasing, within 0 .. T.

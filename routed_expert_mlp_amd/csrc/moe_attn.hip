@@ -21,6 +21,8 @@ using namespace moe;
 
 constexpr int64_t kInt32End = int64_t(1) << 31;
 constexpr int64_t kMaxTokens = int64_t(1) << 26;   // rows of one call
+constexpr int64_t kMaxKeys = int64_t(1) << 30;     // no sequence is as long: as good as no limit
+constexpr int64_t kMaxThreads = int64_t(1) << 32;  // of a launch, along one side; a grid takes fewer
 
 bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -81,7 +83,7 @@ int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q
   const int st = validate_cfg(c);
   if (st) return st;
   if (T < 0 || T >= kMaxTokens) return MOE_MLP_ERR_BAD_SHAPE;
-  if (B < 0 || max_q < 0 || max_len < 0 || B >= kInt32End || max_q >= kInt32End || max_len >= kInt32End / 2)
+  if (B < 0 || max_q < 0 || max_len < 0 || B >= kInt32End || max_q >= kInt32End || max_len >= kMaxKeys)
     return MOE_MLP_ERR_BAD_SHAPE;
   if (!prefill && (max_q < 1 || max_q > MOE_ATTN_DECODE_MAX_Q)) return MOE_MLP_ERR_BAD_SHAPE;
   if (B && max_q * c->n_heads >= kMaxTokens / B) return MOE_MLP_ERR_BAD_SHAPE;
@@ -92,6 +94,7 @@ int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q
 // head) in blocks of 32 * ct, the visible tiles of 32 keys in parts.
 struct DecodePlan {
   int ct, col_blocks, splits, tiles_per_split;
+  int64_t blocks, join_blocks;
   size_t ws_bytes;
 };
 
@@ -114,6 +117,8 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   tps = tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
   p.tiles_per_split = static_cast<int>(tps);
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  p.blocks = B * c->n_kv_heads * p.col_blocks * p.splits;
+  p.join_blocks = p.splits > 1 ? B * n_q * c->n_heads : 0;
   if (p.splits > 1) p.ws_bytes = size_t(B) * c->n_kv_heads * cols * p.splits * (c->head_dim + 2) * 4;
   return p;
 }
@@ -123,6 +128,7 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
 struct PrefillPlan {
   int64_t col_blocks, tiles;         // tiles: the most that a column block can see
   int splits, tiles_per_split;
+  int64_t blocks, join_blocks;
   size_t ws_bytes;
 };
 
@@ -147,6 +153,8 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   p.tiles = tiles;
   p.tiles_per_split = static_cast<int>(std::max<int64_t>(tps, 1));
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  p.blocks = busy * p.splits;
+  p.join_blocks = p.splits > 1 ? busy * (S::COLS / 16) : 0;
   if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
   return p;
 }
@@ -175,10 +183,9 @@ int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t m
 
 template <int D, int CT>
 int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
-  const int64_t blocks = int64_t(a.B) * a.kv_heads * p.col_blocks * p.splits;
-  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(blocks)), dim3(ATTN_NW * 64), s, a);
+  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(p.blocks)), dim3(ATTN_NW * 64), s, a);
   if (st || p.splits == 1) return st;
-  return launch(k_attn_join<D>, dim3(static_cast<unsigned>(int64_t(a.B) * a.n_q * a.heads)), dim3(256), s, a);
+  return launch(k_attn_join<D>, dim3(static_cast<unsigned>(p.join_blocks)), dim3(256), s, a);
 }
 
 int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t T, const int32_t* cu_q,
@@ -217,8 +224,8 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
   a.kv_heads = c->n_kv_heads;
   a.group = c->n_heads / c->n_kv_heads;
   a.page_shift = page_shift_of(c->page_size);
-  a.window = c->window;
-  a.sinks = c->n_sinks;
+  a.window = static_cast<int32_t>(std::min<int64_t>(c->window, kMaxKeys));
+  a.sinks = static_cast<int32_t>(std::min<int64_t>(c->n_sinks, kMaxKeys));
   a.scale_log2 = c->scale * 1.44269504088896340736f;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!prefill) {
@@ -238,10 +245,9 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
     a.splits = p.splits;
     a.tiles_per_split = p.tiles_per_split;
     a.col_blocks = static_cast<int32_t>(p.col_blocks);
-    const int64_t blocks = p.col_blocks * a.kv_heads;
-    const int st = launch(k_attn_prefill<D, NW>, dim3(static_cast<unsigned>(blocks * p.splits)), dim3(NW * 64), s, a);
+    const int st = launch(k_attn_prefill<D, NW>, dim3(static_cast<unsigned>(p.blocks)), dim3(NW * 64), s, a);
     if (st || p.splits == 1) return st;
-    return launch(k_attn_prefill_join<D, NW>, dim3(static_cast<unsigned>(blocks * (2 * NW))), dim3(256), s, a);
+    return launch(k_attn_prefill_join<D, NW>, dim3(static_cast<unsigned>(p.join_blocks)), dim3(256), s, a);
   });
 }
 
@@ -305,11 +311,18 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, in
   if (st) return st;
   if (!bytes) return MOE_MLP_ERR_NULL_ARG;
   if (!prefill) {
-    *bytes = decode_plan(cfg, B, max_q, max_len).ws_bytes;
+    const DecodePlan p = decode_plan(cfg, B, max_q, max_len);
+    if (p.blocks >= kMaxThreads / (ATTN_NW * 64) || p.join_blocks >= kMaxThreads / 256)
+      return MOE_MLP_ERR_BAD_SHAPE;
+    *bytes = p.ws_bytes;
     return MOE_MLP_OK;
   }
-  return with_prefill_shape(cfg, T, B, max_q, max_len, [&](auto dc, auto nc) {
-    *bytes = prefill_plan<decltype(dc)::value, decltype(nc)::value>(cfg, T, B, max_q, max_len).ws_bytes;
+  return with_prefill_shape(cfg, T, B, max_q, max_len, [&](auto dc, auto nc) -> int {
+    constexpr int NW = decltype(nc)::value;
+    const PrefillPlan p = prefill_plan<decltype(dc)::value, NW>(cfg, T, B, max_q, max_len);
+    if (p.col_blocks >= kInt32End || p.blocks >= kMaxThreads / (NW * 64) || p.join_blocks >= kMaxThreads / 256)
+      return MOE_MLP_ERR_BAD_SHAPE;
+    *bytes = p.ws_bytes;
     return MOE_MLP_OK;
   });
 }
