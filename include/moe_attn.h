@@ -130,10 +130,9 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
                     int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
- * The same (here the weights' sum is that of the rounded ones) for prompts, or
- * pieces of prompts behind a cached prefix: sequence b has the new tokens
- * cu_q[b] .. cu_q[b+1]-1 of q, the last ones of its seq_lens[b] tokens, all of
- * them in the cache already.
+ * The same for prompts, or pieces of prompts behind a cached prefix: sequence
+ * b has the new tokens cu_q[b] .. cu_q[b+1]-1 of q, the last ones of its
+ * seq_lens[b] tokens, all of them in the cache already.
  *   q         [T, n_heads, head_dim] bf16;  out the same shape (rows outside
  *             cu_q[0] .. cu_q[B] are not written).
  *   cu_q      [B + 1] int32, not decreasing, within 0 .. T.

@@ -1,26 +1,43 @@
 // Causal attention of prompts over the paged cache.
 //
+//   out = sum_k p_k v_k / sum_k p_k,  p_k = exp2(c q.k - m),  c = scale log2(e)
+//
+// with the running maximum m per query, in one pass over the keys.
+//
 // What bounds it: 4 D flops per query head and visible key on the matrix
-// cores; the softmax's exponentials, conversions and sums take the vector
-// units nearly as long, so the two have to run at once.
+// cores.  The softmax's exponentials, conversions and sums take the vector
+// units nearly as long, so the two have to run at once; and the operands of
+// every matrix instruction come from LDS at about the rate that it has.
 //   * A wavefront owns 32 columns (query rows of one key/value head: new
 //     token x head of the group, the head running faster, so that a key tile
-//     serves the whole group) and a block NW of them.
-//   * Tiles of keys go from the cache to LDS by DMA, in rings of 4 slots for
-//     K and for V, in the cache's own order: operand fragments are then
+//     serves the whole group) and a block NW of them.  64 columns a wavefront
+//     would halve the reads of LDS, but their sums and weights do not fit its
+//     registers (4096 tokens 271 us, copying them to and fro).
+//   * Tiles of keys go from the cache to LDS by DMA, in rings of 2 slots for K
+//     and 4 for V, in the cache's own order: operand fragments are then
 //     consecutive 16 bytes a lane, free of bank conflicts, and nothing is
-//     transposed.
+//     transposed.  (Rings of 4 and 4: the same times.)
 //   * Scores are computed transposed (attn.hpp), so the weights go from the
 //     softmax back into the matrix unit without leaving the lane.
 //   * One iteration computes the scores of tile t + 1 while the vector units
 //     turn those of tile t into weights (phase A), then adds tile t's
-//     weighted values while they look for tile t + 1's maximum (phase B); the
-//     sums are rescaled only when a maximum rises by more than 2^8.
+//     weighted values while they finish that and look for tile t + 1's maximum
+//     (phase B); the sums are rescaled only when a maximum rises by more than
+//     2^8.  There is one barrier a tile.
+//   * Fragments are read four matrix instructions ahead of their use, across
+//     the barrier.  The transfers are buffer loads: behind global ones the
+//     compiler waits for all reads of LDS at every fragment.
 //   * With few columns and a long cache (a piece of a prompt far into its
 //     sequence) the key tiles are cut into parts, a block each, which
 //     k_attn_prefill_join adds up.
-//   * Fragments are read in groups of four, a group ahead of its use and
-//     across the barrier between the phases.
+//
+// Measured, 32 query and 8 key/value heads of 128 dims: 4096 tokens 128-130 us,
+// 1.06-1.08 PFLOP/s, where a large library matrix product reaches 1.2-1.4; the
+// chip is at its power limit then (2.1 of 2.4 GHz), and leaving out the
+// transfers, the LDS reads or the exponentials each changes the time by less
+// than 10%.  Window of 1024 and 4 sinks on 8192 tokens: 153 us, 840 TFLOP/s of
+// visible pairs; a block then visits 35 tiles for the 32 that a query sees, and
+// starts and ends too often to hide that.
 #pragma once
 
 #include "attn.hpp"
@@ -31,6 +48,7 @@ namespace moe {
 
 constexpr int PF_RING = 4;           // slots for values
 constexpr int PF_KRING = 2;          // slots for keys
+constexpr int PF_AHEAD = 4;          // matrix instructions between a fragment's read and its use
 constexpr int PF_IDS = 64;           // tiles whose page ids are in LDS, in two halves
 
 template <int D, int NW_>
@@ -79,6 +97,14 @@ __device__ __forceinline__ bool prefill_block(const AttnArgs& a, int r, int& b, 
   return false;
 }
 
+// The same for every lane, and kept in a scalar register: computed again in a
+// branch that not all lanes take, it would come out of it in a vector register.
+__device__ __forceinline__ int scalar(int v) {
+  v = uniform(v);
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
 // Weights may exceed the running maximum by this many powers of two before
 // the sums are rescaled (fp32 sums and bf16 weights have the range).
 constexpr float PF_SLACK = 8.0f;
@@ -87,12 +113,16 @@ template <int D, int NW>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
   constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS;
   constexpr int RING = PF_RING, KRING = PF_KRING, KS = D / 16, DT = D / 32, SUB = TS / 32;
-  constexpr int NGA = SUB * KS / 4, NGB = 2 * SUB * DT / 4;      // groups of 4 matrix instructions of the two phases
-  static_assert(NGA % 2 == 0 && NGB % 2 == 0, "fragment buffers alternate");
+  constexpr int AHEAD = PF_AHEAD;
   constexpr int NP = 8 * SUB;                                    // pairs of scores of a lane
-  constexpr int NSA = 4 * NGA, NSB = 4 * NGB;                    // steps
-  constexpr int PA = NP > NSA ? NP / NSA : 1, SA = NP > NSA ? 1 : NSA / NP;   // pairs a step, steps a pair
-  constexpr int PB = NP > NSB ? NP / NSB : 1, SB = NP > NSB ? 1 : NSB / NP;
+  constexpr int NSA = SUB * KS, NSB = 2 * SUB * DT;              // steps (matrix instructions) of the two phases
+  static_assert(NSA % AHEAD == 0 && NSB % AHEAD == 0, "fragment i has register i % AHEAD");
+  // Pairs that phase A turns into weights; phase B does the rest before step
+  // LB, where the last 16 keys' values begin, and looks for the maximum before
+  // step MB.  With more dims the matrix instructions of both phases hide the
+  // softmax better than those of one (4096 tokens: 132 and 129.5 us); with 64
+  // the values wait for the weights instead (8 pieces: 66.2 us this way, 67.0).
+  constexpr int QA = D == 64 ? NP : NP * 5 / 8, LB = NSB - NSB / (2 * SUB), MB = NSB * 3 / 4;
   // key/value heads run fastest over the blocks: with a multiple of 8 of them
   // the blocks of one stay on one XCD, whose L2 then holds its keys
   const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads, split = bi / a.col_blocks;
@@ -108,6 +138,12 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
   const bool whole = tl.n <= a.tiles_per_split;
   if (!tl.keep_part(split, a.tiles_per_split)) return;
+  const int last = scalar(tl.n - 1), skip = scalar(tl.skip), na = scalar(tl.na), jump = scalar(tl.b0 - tl.na);
+  // first key of tile v of this part; past its end, of the last one
+  auto key_of = [&](int v) __attribute__((always_inline)) {
+    v = min(v, last) + skip;
+    return TS * (v < na ? v : v + jump);
+  };
 
   // slots are arrays of their own, so that the compiler knows which reads a
   // transfer in flight cannot touch
@@ -140,56 +176,57 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   auto load_ids = [&](int first_tile, int n) __attribute__((always_inline)) {
     for (int i = tid; i < TS / 16 * n; i += NW * 64) {
       const int v = first_tile + i / (TS / 16), part = i % (TS / 16);
-      const int key = min(TS * tl.tile(min(v, tl.n - 1)) + 16 * part, s.len - 1);
+      const int key = min(key_of(v) + 16 * part, s.len - 1);
       ids[TS / 16 * (v & (PF_IDS - 1)) + part] =
           min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);          // the writes have been done (lgkmcnt 0)
   };
+  // Transfers: 64 pieces of 16 bytes to consecutive places of a slot, out of one
+  // page, whose address is the same for all lanes.
   using lds_t = void __attribute__((address_space(3)));
   constexpr int NI = TS * D / 8 / 64 / NW;       // transfers of a wavefront for a tile's keys, and for its values
-  // K slot: [D / 8][TS keys][16 bytes], row l of it key swap23(l % 32) of its 32
-  constexpr int CPI = 64 / TS;                   // chunks of 8 dims a transfer
-  const int lkey = TS == 64 ? 32 * half + swap23(r) : swap23(r);
-  const int lchunk = CPI * w + (TS == 64 ? 0 : half);
-  const uint64_t kbase = reinterpret_cast<uint64_t>(a.k) + static_cast<uint64_t>(kvh) * head_bytes +
-                         ((lchunk << a.page_shift) + (lkey & (ps - 1))) * 16;
+  auto bring = [&](const uint16_t* base, int id, int at, int lane_at, int step, uint4* dst) __attribute__((always_inline)) {
+    const uint64_t src = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes +
+                         static_cast<uint64_t>(kvh) * head_bytes + static_cast<uint32_t>(at);
+    const uint64_t one = static_cast<uint32_t>(uniform(static_cast<uint32_t>(src))) |
+                         static_cast<uint64_t>(static_cast<uint32_t>(uniform(static_cast<uint32_t>(src >> 32)))) << 32;
+    const auto page = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(one), 0, head_bytes, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(page, (lds_t*)dst, 16, lane_at, step, 0, 0);
+  };
+  // K slot: [TS / 16][D / 8][16 keys][16 bytes], row j of 16 keys is key
+  // swap23(j); a transfer brings 4 chunks of 8 dims of 16 keys, a wavefront's
+  // are of the same keys
+  constexpr int PER16 = D / 32;                  // transfers for 16 keys
+  static_assert(PER16 % NI == 0, "one page a wavefront");
+  const int kgroup = w * NI / PER16, kchunk = 4 * (w * NI % PER16);
+  const int klane = (((kchunk + (lane >> 4)) << a.page_shift) + swap23(lane & 15)) * 16;
   auto key_page = [&](int v) __attribute__((always_inline)) {
-    return ids[TS / 16 * (min(v, tl.n - 1) & (PF_IDS - 1)) + (lkey >> 4)];
+    return ids[TS / 16 * (min(v, last) & (PF_IDS - 1)) + kgroup];
   };
-  auto key_source = [&](int v, int id) __attribute__((always_inline)) {
-    return static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes + kbase +
-           static_cast<uint32_t>((TS * tl.tile(min(v, tl.n - 1))) & (ps - 1)) * 16;
-  };
-  auto issue_k = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
-    __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + ((CPI * NW * i * 16) << a.page_shift)),
-                                     (lds_t*)(slot + (NW * i + w) * 64), 16, 0, 0);
+  auto issue_k = [&](int v, int id, uint4* slot, int i) __attribute__((always_inline)) {
+    bring(a.k, id, ((key_of(v) + 16 * kgroup) & (ps - 1)) * 16, klane, (64 * i) << a.page_shift,
+          slot + (NI * w + i) * 64);
   };
   // V slot: [TS / 8][D][16 bytes]; wavefront w brings keys TS / NW * w and on, all of one page
   constexpr int WK = TS / NW;
-  const uint64_t vbase = reinterpret_cast<uint64_t>(a.v) + static_cast<uint64_t>(kvh) * head_bytes +
-                         ((WK * w) & (ps - 1)) * (2 * D) + lane * 16;
   auto value_page = [&](int v) __attribute__((always_inline)) {
-    return ids[TS / 16 * (min(v, tl.n - 1) & (PF_IDS - 1)) + (WK * w >> 4)];
+    return ids[TS / 16 * (min(v, last) & (PF_IDS - 1)) + (WK * w >> 4)];
   };
-  auto value_source = [&](int v, int id) __attribute__((always_inline)) {
-    return static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes + vbase +
-           static_cast<uint32_t>((TS * tl.tile(min(v, tl.n - 1))) & (ps - 1)) * (2 * D);
-  };
-  auto issue_v = [&](uint64_t p, uint4* slot, int i) __attribute__((always_inline)) {
-    __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(p + 1024 * i),
-                                     (lds_t*)(slot + WK / 8 * D * w + 64 * i), 16, 0, 0);
+  auto issue_v = [&](int v, int id, uint4* slot, int i) __attribute__((always_inline)) {
+    bring(a.v, id, ((key_of(v) + WK * w) & (ps - 1)) * (2 * D), lane * 16, 1024 * i,
+          slot + (NI * w + i) * 64);
   };
   auto all_k = [&](int v) __attribute__((always_inline)) {
-    const uint64_t p = key_source(v, key_page(v));
+    const int id = uniform(key_page(v));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) issue_k(p, kslot[v % KRING], i);
+    for (int i = 0; i < NI; ++i) issue_k(v, id, kslot[v % KRING], i);
   };
   auto all_v = [&](int v) __attribute__((always_inline)) {
-    const uint64_t p = value_source(v, value_page(v));
+    const int id = uniform(value_page(v));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) issue_v(p, vslot[v], i);
+    for (int i = 0; i < NI; ++i) issue_v(v, id, vslot[v], i);
   };
   // Waits for this wavefront's transfers but the VM latest, then for the other
   // wavefronts to be here too.
@@ -209,7 +246,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
 
   // scores of invisible keys to -inf, where the tile has some for this wavefront
   auto mask = [&](int v, f32x16 (&x)[SUB]) __attribute__((always_inline)) {
-    const int key0 = TS * tl.tile(v);
+    const int key0 = key_of(v);
     if (key0 + TS - 1 <= wp_first && (key0 >= wlo_last || key0 + TS <= tl.sinks)) return;
     const int pos = first + col / a.group;
     const uint64_t see = visible_bits(key0 + 8 * half, pos, attn_window_lo(a, pos), tl.sinks);
@@ -219,9 +256,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
       for (int e = 0; e < 16; ++e)
         x[sub][e] = keep_if(static_cast<uint32_t>(see >> (32 * sub)), 16 * (e >> 3) + (e & 7), x[sub][e]);
   };
-  // new maximum (mx: this lane's largest score), and the sums rescaled if it rose enough
-  auto rescale = [&](float mx) __attribute__((always_inline)) {
-    const float mt = max_halves(mx) * a.scale_log2;
+  // new maximum (mt: the largest score of the tile), and the sums rescaled if it rose enough
+  auto rescale = [&](float mt) __attribute__((always_inline)) {
     if (__builtin_expect(!__any(mt > m + PF_SLACK), 1)) return;
     const float mn = fmaxf(m, mt);
     const float f = exp2_fast(m - mn);
@@ -234,27 +270,22 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   };
   // values of keys that no column sees, whatever their slots hold, to 0 (all wavefronts)
   auto clear_holes = [&](int v, uint4* slot) __attribute__((always_inline)) {
-    const int key0 = TS * tl.tile(v);
+    const int key0 = key_of(v);
     if (key0 + TS <= tl.hi && (key0 >= tl.lo || key0 + TS <= tl.sinks)) return;
     for (int i = tid; i < TS * D / 8; i += NW * 64)
       slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(visible_bits(key0 + 8 * (i / D), tl.hi - 1, tl.lo, tl.sinks))));
     __syncthreads();
   };
-  // Group g of 4 fragments of a K slot (32 keys, then 16 dims on) or V slot (16 keys, then 32 dims on).
-  bf16x8 fr[2][4];
-  auto read_k = [&](const uint4* slot, int g, bf16x8 (&f)[4]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 4 * g + j;
-      f[j] = __builtin_bit_cast(bf16x8, slot[(2 * (i % KS) + half) * TS + 32 * (i / KS) + r]);
-    }
+  // Fragment i of a K slot (32 keys, then 16 dims on) or V slot (16 keys, then 32 dims on).
+  bf16x8 fr[AHEAD];
+  auto key_at = [&](int i) __attribute__((always_inline)) {
+    return (r >> 4) * (2 * D) + 16 * half + (r & 15) + i / KS * (4 * D) + 32 * (i % KS);
   };
-  auto read_v = [&](const uint4* slot, int g, bf16x8 (&f)[4]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 4 * g + j;
-      f[j] = __builtin_bit_cast(bf16x8, slot[(2 * (i / DT) + half) * D + 32 * (i % DT) + r]);
-    }
+  auto read_k = [&](const uint4* slot, int i) __attribute__((always_inline)) {
+    fr[i % AHEAD] = __builtin_bit_cast(bf16x8, slot[key_at(i)]);
+  };
+  auto read_v = [&](const uint4* slot, int i) __attribute__((always_inline)) {
+    fr[i % AHEAD] = __builtin_bit_cast(bf16x8, slot[(2 * (i / DT) + half) * D + 32 * (i % DT) + r]);
   };
   int kid = 0, vid = 0;          // pages of the keys and values to bring next
   // Pair p of the scores to weights, their sum to l.
@@ -264,7 +295,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     const float p0 = exp2_fast(fmaf(x[su][e], a.scale_log2, -m));
     const float p1 = exp2_fast(fmaf(x[su][e + 1], a.scale_log2, -m));
     uint32_t pp = pack_bf16x2(p0, p1);
-    l = dot2_bf16(pp, 0x3F803F80u, l);
+    l += p0 + p1;
     asm volatile("" : "+v"(pp), "+v"(l));        // here, beside the matrix instructions, and not where it is used
     pk[2 * su + (e >> 3)][(e & 7) >> 1] = pp;
   };
@@ -284,16 +315,13 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     constexpr int GAP = NSB / (2 * NI) < 3 ? NSB / (2 * NI) : 3;   // steps between transfers
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
-      const int g = i / 4, sub = i / KS;
+      const int sub = i / KS;
       f32x16 z = {};
-      y[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], qf[i % KS], i % KS ? y[sub] : z, 0, 0, 0);
-      if (i % 4 == 0) {
-        if (g + 1 < NGA) read_k(kslot[(J + 1) % KRING], g + 1, fr[(g + 1) & 1]);
-        else read_v(vslot[J], 0, fr[0]);
-      }
+      y[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % AHEAD], qf[i % KS], i % KS ? y[sub] : z, 0, 0, 0);
+      if (i + AHEAD < NSA) read_k(kslot[(J + 1) % KRING], i + AHEAD);
+      else read_v(vslot[J], i + AHEAD - NSA);
 #pragma unroll
-      for (int j = 0; j < PA; ++j)
-        if (i % SA == 0) weigh(i / SA * PA + j, x);
+      for (int p = i * QA / NSA; p < (i + 1) * QA / NSA; ++p) weigh(p, x);
       __builtin_amdgcn_sched_barrier(0);
     }
     arrive(std::integral_constant<int, NI>{});
@@ -302,50 +330,46 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
       mask(t + 1, y);
     }
     float mx = y[0][0];
-    uint64_t ksrc = 0, vsrc = 0;
+    const int kpage = uniform(kid), vpage = uniform(vid);
 #pragma unroll
     for (int i = 0; i < NSB; ++i) {
-      const int g = i / 4;
-      acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], weights(i / DT), acc[i % DT], 0, 0, 0);
-      if (i % 4 == 0) {
-        if (g + 1 < NGB) read_v(vslot[J], g + 1, fr[(g + 1) & 1]);
-        else read_k(kslot[J % KRING], 0, fr[0]);
-      }
-      if (i == 0) ksrc = key_source(t + 3, kid);
-      if (i == NI * GAP) vsrc = value_source(t + 3, vid);
-      if (i % GAP == GAP - 1 && i / GAP < NI) issue_k(ksrc, kslot[(J + 1) % KRING], i / GAP);
-      if (i % GAP == GAP - 1 && i / GAP >= NI && i / GAP < 2 * NI) issue_v(vsrc, vslot[(J + 3) % RING], i / GAP - NI);
+      acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % AHEAD], weights(i / DT), acc[i % DT], 0, 0, 0);
+      if (i + AHEAD < NSB) read_v(vslot[J], i + AHEAD);
+      else read_k(kslot[J % KRING], i + AHEAD - NSB);
+      if (i % GAP == GAP - 1 && i / GAP < NI) issue_k(t + 3, kpage, kslot[(J + 1) % KRING], i / GAP);
+      if (i % GAP == GAP - 1 && i / GAP >= NI && i / GAP < 2 * NI) issue_v(t + 3, vpage, vslot[(J + 3) % RING], i / GAP - NI);
       if (i == NSB - 1) {
         kid = key_page(t + 4);
         vid = value_page(t + 4);
       }
 #pragma unroll
-      for (int j = 0; j < PB; ++j)
-        if (i % SB == 0) {
-          const int p = i / SB * PB + j, su = p >> 3, e = 2 * (p & 7);
-          mx = fmaxf(fmaxf(mx, y[su][e]), y[su][e + 1]);
-          asm volatile("" : "+v"(mx));
-        }
+      for (int p = QA + min(i, LB) * (NP - QA) / LB; p < QA + min(i + 1, LB) * (NP - QA) / LB; ++p) weigh(p, x);
+#pragma unroll
+      for (int p = min(i, MB) * NP / MB; p < min(i + 1, MB) * NP / MB; ++p) {
+        const int su = p >> 3, e = 2 * (p & 7);
+        mx = fmaxf(fmaxf(mx, y[su][e]), y[su][e + 1]);
+        asm volatile("" : "+v"(mx));
+      }
+      if (i == MB) mx = max_halves(mx) * a.scale_log2;
       __builtin_amdgcn_sched_barrier(0);
     }
     rescale(mx);
   };
 
-  if (tl.n > 0) {
+  if (last >= 0) {
     load_ids(0, PF_IDS);
     __syncthreads();
     all_k(0);
-    if (tl.n > 1) all_k(1);
+    all_k(1);
     all_v(0);
-    if (tl.n > 1) all_v(1);
+    all_v(1);
     kid = key_page(3);
     vid = value_page(3);
-    if (tl.n > 1) arrive(std::integral_constant<int, 3 * NI>{});
-    else arrive(std::integral_constant<int, NI>{});
+    arrive(std::integral_constant<int, 3 * NI>{});
 #pragma unroll
     for (int i = 0; i < NSA; ++i) {
       f32x16 z = {};
-      const bf16x8 f = __builtin_bit_cast(bf16x8, k0[(2 * (i % KS) + half) * TS + 32 * (i / KS) + r]);
+      const bf16x8 f = __builtin_bit_cast(bf16x8, k0[key_at(i)]);
       sa[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[i % KS], i % KS ? sa[i / KS] : z, 0, 0, 0);
     }
     mask(0, sa);
@@ -354,16 +378,16 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     for (int su = 0; su < SUB; ++su)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sa[su][e]);
-    rescale(mx);
-    if (tl.n > 1) arrive(std::integral_constant<int, NI>{});
-    else arrive(std::integral_constant<int, 0>{});
-    if (tl.n > 1) {
-      all_k(2);
-      all_v(2);
-    }
+    rescale(max_halves(mx) * a.scale_log2);
+    arrive(std::integral_constant<int, NI>{});   // and everyone is past its reads of the keys of tile 0
+    all_k(2);
+    all_v(2);
     clear_holes(0, v0);
-    read_k(k1, 0, fr[0]);
-    const int last = tl.n - 1;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      read_k(k1, i);
+      __builtin_amdgcn_sched_barrier(0);         // in this order, which the waits in the loop count on
+    }
     for (int t = 0; t < last; t += RING) {
       if (__builtin_expect(t % (PF_IDS / 2) == 0 && t, 0)) load_ids(t + PF_IDS / 2, PF_IDS / 2);
       iteration(std::integral_constant<int, 0>{}, t, sa, sb);
@@ -385,11 +409,11 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     const int j = last % RING;
     const uint4* vl = j == 0 ? v0 : j == 1 ? v1 : j == 2 ? v2 : v3;
 #pragma unroll
-    for (int g = 0; g < NGB; ++g) {
-      read_v(vl, g, fr[g & 1]);
+    for (int i = 0; i < AHEAD; ++i) read_v(vl, i);
 #pragma unroll
-      for (int i = 4 * g; i < 4 * g + 4; ++i)
-        acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[g & 1][i % 4], weights(i / DT), acc[i % DT], 0, 0, 0);
+    for (int i = 0; i < NSB; ++i) {
+      acc[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr[i % AHEAD], weights(i / DT), acc[i % DT], 0, 0, 0);
+      if (i + AHEAD < NSB) read_v(vl, i + AHEAD);
     }
   }
 
