@@ -16,12 +16,17 @@
 //   * one block is 4 wavefronts that take tiles of 32 keys in turn, each with
 //     its next tile's keys and values in flight while it works on the present
 //     one; they join their parts in LDS.  Two blocks share a CU (at 128 dims),
-//     so that one streams while the other starts or joins: 131071 keys of 8
-//     key/value heads in 512 parts 100 us, against 106 us with one block of 8;
+//     so that one streams while the other starts or joins (one block of 8: 106 us
+//     where this took 100);
 //   * the visible tiles of a sequence are cut into parts of tiles_per_split,
 //     a block each; a sequence with one part is done by then, the others'
 //     parts (unnormalised sums, maximum and sum, in fp32) are joined by
 //     k_attn_join.
+//
+// Measured, 32 query and 8 key/value heads of 128 dims: one token over 131071 keys
+// 87 us, 6.2 TB/s (a large copy reaches 4.8 TB/s, reads and writes together); 64
+// sequences of 1..8192 keys 179 us, 6.0 TB/s; 777 keys 8.4 us, which is two
+// launches that wait for one load after the other.
 #pragma once
 
 #include "attn.hpp"
@@ -285,19 +290,25 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
   }
 }
 
-// Joins the parts of one output row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// Joins the parts of an output row: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // Lane i of every wavefront has part i's maximum and sum (64 parts at a time),
-// so that M and the factors are known after one load; then the four wavefronts
-// add up every fourth part, D / 64 dims a lane, with several loads in flight.
-template <int D>
+// so that M and the factors are known after one load; then the RW wavefronts of
+// a row add up every RW'th part, D / 64 dims a lane, with several loads in
+// flight.  Few rows have 4 wavefronts each, which join in LDS (one token over
+// 131071 keys, 32 rows of 64 parts: 86.9 us in all, and 89.5 us with one); 1024
+// rows or more have one each, in a quarter of the blocks (2048 rows of at most 7
+// parts of 64 dims: 19.6 us in all, and 21.1 us with 4).
+template <int D, int RW>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int ND = D / 64, UNROLL = 4;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int cols = a.n_q * a.group;
-  const int col = blockIdx.x % cols, kvh = (blockIdx.x / cols) % a.kv_heads, b = blockIdx.x / cols / a.kv_heads;
+  const int row = blockIdx.x * (4 / RW) + w / RW;
+  const int col = row % cols, kvh = (row / cols) % a.kv_heads, b = row / cols / a.kv_heads;
+  if (RW == 1 && b >= a.B) return;
   const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits;
   const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
   const float2* ml = reinterpret_cast<const float2*>(a.ws + items * D) + item;
-  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const float* const sums = a.ws + item * D + lane * ND;
   // asked for before the sequence's length is known: whether it has that part or not
   const float2 first_ml = ml[min(lane, a.splits - 1)];
@@ -318,25 +329,35 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     L = L * old + wave_sum(lane < here ? p.y * f : 0.0f);
 #pragma unroll
     for (int n = 0; n < ND; ++n) o[n] *= old;
-    for (int i0 = w; i0 < here; i0 += 4 * UNROLL) {
+    for (int i0 = w % RW; i0 < here; i0 += RW * UNROLL) {
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
-        const int i = min(i0 + 4 * u, here - 1);
-        const float g = i0 + 4 * u < here ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i)) : 0.0f;
+        const int i = min(i0 + RW * u, here - 1);
+        const float g = i0 + RW * u < here ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i)) : 0.0f;
         const float* src = sums + static_cast<int64_t>(p0 + i) * D;
 #pragma unroll
         for (int n = 0; n < ND; ++n) o[n] += src[n] * g;
       }
     }
   }
-  __shared__ float lo_[4][D];
-#pragma unroll
-  for (int n = 0; n < ND; ++n) lo_[w][lane * ND + n] = o[n];
-  __syncthreads();
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   uint16_t* out = a.out + attn_row(a, s.row0, kvh, col) * D;
-  for (int d = threadIdx.x; d < D; d += 256)
-    out[d] = f32_to_bf16(((lo_[0][d] + lo_[1][d]) + (lo_[2][d] + lo_[3][d])) * inv);
+  if constexpr (RW == 1) {
+    if constexpr (ND == 1) {
+      out[lane] = f32_to_bf16(o[0] * inv);
+    } else {
+#pragma unroll
+      for (int n = 0; n < ND; n += 2)
+        *reinterpret_cast<uint32_t*>(out + lane * ND + n) = pack_bf16x2(o[n] * inv, o[n + 1] * inv);
+    }
+  } else {
+    __shared__ float lo_[4][D];
+#pragma unroll
+    for (int n = 0; n < ND; ++n) lo_[w][lane * ND + n] = o[n];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256)
+      out[d] = f32_to_bf16(((lo_[0][d] + lo_[1][d]) + (lo_[2][d] + lo_[3][d])) * inv);
+  }
 }
 
 }  // namespace moe

@@ -94,6 +94,7 @@ int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q
 // head) in blocks of 32 * ct, the visible tiles of 32 keys in parts.
 struct DecodePlan {
   int ct, col_blocks, splits, tiles_per_split;
+  int join_waves;                    // of an output row of the join
   int64_t blocks, join_blocks;
   size_t ws_bytes;
 };
@@ -118,7 +119,9 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   p.tiles_per_split = static_cast<int>(tps);
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
   p.blocks = B * c->n_kv_heads * p.col_blocks * p.splits;
-  p.join_blocks = p.splits > 1 ? B * n_q * c->n_heads : 0;
+  const int64_t rows = B * n_q * c->n_heads;
+  p.join_waves = rows < 1024 ? 4 : 1;            // measured at k_attn_join
+  p.join_blocks = p.splits > 1 ? cdiv(rows, 4 / p.join_waves) : 0;
   if (p.splits > 1) p.ws_bytes = size_t(B) * c->n_kv_heads * cols * p.splits * (c->head_dim + 2) * 4;
   return p;
 }
@@ -185,7 +188,9 @@ template <int D, int CT>
 int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
   const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(p.blocks)), dim3(ATTN_NW * 64), s, a);
   if (st || p.splits == 1) return st;
-  return launch(k_attn_join<D>, dim3(static_cast<unsigned>(p.join_blocks)), dim3(256), s, a);
+  const dim3 grid(static_cast<unsigned>(p.join_blocks));
+  return p.join_waves == 1 ? launch(k_attn_join<D, 1>, grid, dim3(256), s, a)
+                           : launch(k_attn_join<D, 4>, grid, dim3(256), s, a);
 }
 
 int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t T, const int32_t* cu_q,

@@ -94,6 +94,17 @@ def test_decode(heads, kv, dim, page, new, lens, window, sinks):
     check(b, run_decode(b), what)
 
 
+@pytest.mark.parametrize("heads,kv,dim,new,window", [(32, 8, 64, 1, 0), (32, 8, 128, 1, 0), (16, 4, 128, 2, 700),
+                                                     (32, 4, 256, 1, 0)])
+def test_decode_many_rows(heads, kv, dim, new, window):
+    """A thousand rows and more, of sequences with no key, one part and several."""
+    rng = np.random.default_rng(dim + new)
+    lens = [0, 1, 31, 1400, 129] + [int(n) for n in rng.integers(1, 1200, 35)]
+    b = make_batch(config(heads, kv, dim, 32, window=window, sinks=2), lens, [new] * len(lens), seed=dim)
+    print(f"[case] decode of {len(lens) * new * heads} rows of {dim} dims, window {window}", flush=True)
+    check(b, run_decode(b), f"decode, many rows of {dim} dims")
+
+
 def test_decode_bound_on_length_above_and_below():
     """max_len far above the lengths changes nothing; below, sequences are cut to it."""
     cfg = config(8, 2, 128, 16)
