@@ -33,9 +33,9 @@
 //
 // Measured, 32 query and 8 key/value heads of 128 dims: 4096 tokens 128-130 us,
 // 1.06-1.08 PFLOP/s, where a large library matrix product reaches 1.2-1.4; the
-// chip is at its power limit then (2.1 of 2.4 GHz), and leaving out the
-// transfers, the LDS reads or the exponentials each changes the time by less
-// than 10%.  Window of 1024 and 4 sinks on 8192 tokens: 153 us, 840 TFLOP/s of
+// chip is at its power limit then (2.1 of 2.4 GHz).  Left out one after the
+// other, the exponentials take 7% of that, the maximum 2%, the transfers 3% and
+// the reads of LDS 17%; the rest is the products.  Window of 1024 and 4 sinks on 8192 tokens: 153 us, 840 TFLOP/s of
 // visible pairs; a block then visits 35 tiles for the 32 that a query sees, and
 // starts and ends too often to hide that.
 #pragma once

@@ -102,13 +102,20 @@ struct DecodePlan {
 DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len) {
   DecodePlan p{};
   const int64_t cols = n_q * (c->n_heads / c->n_kv_heads);
-  p.ct = cols > 32 && c->head_dim != 256 ? 2 : 1;
-  p.col_blocks = static_cast<int>(cdiv(cols, 32 * p.ct));
   int64_t tiles = cdiv(max_len, 32);
   if (c->window) {
     const int64_t seen = cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32);
     if (seen < tiles) tiles = seen;
   }
+  // 64 columns a block where reading the keys and values again for every 32
+  // would be more than 56 MB; below that more and smaller blocks are faster.  64
+  // columns of 128 dims, 16 key/value heads in all: 2000 keys 24.7 us, and 30.6
+  // us with 32 columns a block; 2 heads in all and 3000 keys: 13.4 and 9.9 us;
+  // 64 dims, 16 heads in all: 16000 keys 24.0 and 27.6 us, 4000 keys 17.8 and
+  // 13.8 us.  At 256 dims the sums of 64 columns would not fit the registers.
+  const int64_t again = B * c->n_kv_heads * cdiv(cols, 32) * tiles;      // tiles of 128 * head_dim bytes
+  p.ct = cols > 32 && c->head_dim != 256 && again > (int64_t(56) << 20) / (128 * c->head_dim) ? 2 : 1;
+  p.col_blocks = static_cast<int>(cdiv(cols, 32 * p.ct));
   // parts that together fill the places of the GPU's 256 CUs once, if all
   // sequences were as long as the longest may be; no smaller than a tile per
   // wavefront, and no larger than ATTN_MAX_TPS, since the others should not
@@ -148,9 +155,9 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
     tiles = std::min(tiles, cdiv(int64_t(c->window) + cdiv(S::COLS, group), S::TS) + 1 + cdiv(c->n_sinks, S::TS));
   // Parts only where the blocks leave most places of the 256 CUs empty, and
   // then one part a place, if all were as long as the longest may be.  512
-  // tokens behind 65024 cached ones (66 blocks of 32/8 heads of 128 dims): 530
-  // us in parts, 1360 us whole; 16 behind 8176: 42 and 168 us; but 8 pieces
-  // behind prefixes, 456 blocks for 512 places: 121 us in parts, 105 us whole.
+  // tokens behind 65024 cached ones (66 blocks of 32/8 heads of 128 dims): 481
+  // us in parts, 1255 us whole; 16 behind 8176: 22 and 156 us; but 8 pieces
+  // behind prefixes, 440 blocks for 512 places: 83 us in parts, 74 us whole.
   const int64_t places = 256 * S::PER_CU;
   const int64_t tps = 2 * busy > places ? tiles : std::max<int64_t>(cdiv(busy * tiles, places), 16);
   p.tiles = tiles;
@@ -165,12 +172,13 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
 // Calls f(head_dim, wavefronts of a block) with both as integral constants.  At
 // 128 dims a block has 8 wavefronts, which share a tile's transfers, or 4 with
 // tiles of 32 keys, two blocks a CU, of which one starts or ends while the other
-// computes.  Long blocks want the former (32/8 heads: 4096 tokens 133 us, and
-// 149 us with 4; a window of 4096 on 8192 tokens 403 and 419 us), short ones the
-// latter (2048 tokens 53 us, and 59 us with 8; a window of 1024 on 8192 tokens 169
-// and 179 us), and so do those that leave CUs empty (512 tokens of 16/2 heads
-// behind 4096: 36 and 41 us) unless their parts are long all the same (512
-// tokens of 32/8 heads behind 65024: 612 and 530 us).  Other widths have one form.
+// computes.  Long blocks want the former (32/8 heads: 4096 tokens 139 us, and
+// 150 us with 4; a window of 4096 on 8192 tokens 389 and 397 us), short ones the
+// latter (2048 tokens 50 us, and 54 us with 8; a window of 1024 on 8192 tokens 150
+// and 157 us), and so do those that leave CUs empty (16 tokens behind 8176: 22
+// and 31 us; 512 of 16/2 heads behind 4096 come out alike, 42 and 40 us) unless
+// their parts are long all the same (512 tokens of 32/8 heads behind 65024: 542
+// us with 4, 481 us with 8).  Other widths have one form.
 template <typename F>
 int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
   using four = std::integral_constant<int, 4>;
@@ -303,6 +311,8 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
     constexpr int D = decltype(dc)::value;
     const int64_t token_blocks = cdiv(T, 2048 / D);
     // one head a block while the blocks are few, up to 8 with thousands of them
+    // (4096 tokens of 32/8 heads of 128 dims: 21.7 us, and 26.9 us with one always;
+    // 64 tokens of 64/8 heads: 3.6 us, and 8.1 us with 8 always)
     const int64_t per = rows * token_blocks / PREP_BLOCKS;
     a.rows_per_block = static_cast<int32_t>(per < 1 ? 1 : per > 8 ? 8 : per);
     return launch(k_attn_prepare<D>, dim3(static_cast<unsigned>(token_blocks),

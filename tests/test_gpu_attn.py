@@ -105,6 +105,16 @@ def test_decode_many_rows(heads, kv, dim, new, window):
     check(b, run_decode(b), f"decode, many rows of {dim} dims")
 
 
+@pytest.mark.parametrize("heads,kv,dim,new,window", [(64, 1, 128, 1, 0), (71, 1, 64, 1, 0), (16, 2, 64, 8, 9000),
+                                                     (12, 1, 128, 4, 0)])
+def test_decode_wide_groups(heads, kv, dim, new, window):
+    """More than 32 rows of a key/value head over keys that are worth reading once only."""
+    lens = [16000, 0, 5, 33, 64, 700, 1, 4001, 12, 32, 2050, 8]
+    b = make_batch(config(heads, kv, dim, 64, window=window, sinks=3), lens, [new] * len(lens), seed=heads)
+    print(f"[case] decode of {new * heads // kv} rows a head of {dim} dims, window {window}", flush=True)
+    check(b, run_decode(b), f"decode, wide groups of {dim} dims")
+
+
 def test_decode_bound_on_length_above_and_below():
     """max_len far above the lengths changes nothing; below, sequences are cut to it."""
     cfg = config(8, 2, 128, 16)
