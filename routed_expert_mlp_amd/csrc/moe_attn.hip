@@ -153,16 +153,28 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   int64_t tiles = cdiv(max_len, S::TS);
   if (c->window)
     tiles = std::min(tiles, cdiv(int64_t(c->window) + cdiv(S::COLS, group), S::TS) + 1 + cdiv(c->n_sinks, S::TS));
-  // Parts only where the blocks leave most places of the 256 CUs empty, and
-  // then one part a place, if all were as long as the longest may be.  512
-  // tokens behind 65024 cached ones (66 blocks of 32/8 heads of 128 dims): 481
-  // us in parts, 1255 us whole; 16 behind 8176: 22 and 156 us; but 8 pieces
-  // behind prefixes, 440 blocks for 512 places: 83 us in parts, 74 us whole.
+  // Parts where the longest block's tiles take longer than its parts' and the
+  // join: about TILE_NS a tile, 1.6 times that with two blocks on a CU, and for
+  // the join 4 us and the partial sums' way out and back.  Parts of one size that
+  // have places at once, or as many as there are places if all blocks were as
+  // long as the longest may be; none shorter than 8 tiles.  32/8 heads: 512
+  // tokens behind 65024 cached ones 473 us, and 1255 us whole; 64 behind 7168
+  // 25 and 141 us, behind 1024 14.5 and 23 us; 8 pieces of 8/2 heads of 256 dims
+  // behind prefixes (178 blocks at most) 82 and 116 us; but 1024 tokens of a
+  // prompt 23.4 us whole, and 28.8 us in two parts.
+  constexpr int64_t TILE_NS = D == 64 ? 600 : D == 256 ? 780 : NW == 8 ? 1900 : 550;
   const int64_t places = 256 * S::PER_CU;
-  const int64_t tps = 2 * busy > places ? tiles : std::max<int64_t>(cdiv(busy * tiles, places), 16);
+  int64_t size = tiles, best = tiles * TILE_NS * (busy > 256 ? 8 : 5) / 5;
+  auto consider = [&](int64_t tps) {
+    const int64_t ns = tps * TILE_NS * (busy * tiles > 256 * tps ? 8 : 5) / 5 + 4000 +
+                       T * c->n_heads * cdiv(tiles, tps) * D * 8 / (D == 64 ? 4000 : 6000);
+    if (ns < best) best = ns, size = tps;
+  };
+  for (int64_t n = 2; busy * n <= places && tiles >= 8 * n; n += n / 4 + 1) consider(cdiv(tiles, n));
+  if (busy <= places) consider(std::max<int64_t>(cdiv(busy * tiles, places), 8));
   p.tiles = tiles;
-  p.tiles_per_split = static_cast<int>(std::max<int64_t>(tps, 1));
-  p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  p.tiles_per_split = static_cast<int>(std::max<int64_t>(size, 1));
+  p.splits = tiles ? static_cast<int>(cdiv(tiles, size)) : 1;
   p.blocks = busy * p.splits;
   p.join_blocks = p.splits > 1 ? busy * (S::COLS / 16) : 0;
   if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
@@ -172,13 +184,12 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
 // Calls f(head_dim, wavefronts of a block) with both as integral constants.  At
 // 128 dims a block has 8 wavefronts, which share a tile's transfers, or 4 with
 // tiles of 32 keys, two blocks a CU, of which one starts or ends while the other
-// computes.  Long blocks want the former (32/8 heads: 4096 tokens 139 us, and
-// 150 us with 4; a window of 4096 on 8192 tokens 389 and 397 us), short ones the
-// latter (2048 tokens 50 us, and 54 us with 8; a window of 1024 on 8192 tokens 150
-// and 157 us), and so do those that leave CUs empty (16 tokens behind 8176: 22
-// and 31 us; 512 of 16/2 heads behind 4096 come out alike, 42 and 40 us) unless
-// their parts are long all the same (512 tokens of 32/8 heads behind 65024: 542
-// us with 4, 481 us with 8).  Other widths have one form.
+// computes.  Long blocks that fill the GPU for 16 tiles want the former (32/8
+// heads: 4096 tokens 128 us, and 142 us with 4; 512 tokens behind 65024 470 and
+// 522 us, behind 3072 42.1 and 44.3 us), short or few ones the latter (2048 tokens
+// 48 us, and 53 us with 8; a window of 1024 on 8192 tokens 144 and 154 us; 256
+// tokens behind 3072 27.3 and 30.0 us; 16 behind 8176 23 and 26 us).  Other widths
+// have one form.
 template <typename F>
 int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
   using four = std::integral_constant<int, 4>;
@@ -186,7 +197,7 @@ int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t m
   return with_dim(c->head_dim, [&](auto dc) {
     if constexpr (decltype(dc)::value == 128) {
       const PrefillPlan p = prefill_plan<128, 4>(c, T, B, max_q, max_len);
-      if (p.tiles > 64 && (p.col_blocks * c->n_kv_heads > 256 || p.tiles_per_split > 128)) return f(dc, eight{});
+      if (p.tiles > 64 && p.col_blocks * c->n_kv_heads * p.tiles > 16 * 512) return f(dc, eight{});
     }
     return f(dc, four{});
   });
