@@ -18,7 +18,11 @@
 //     8 store their values one by one.
 //
 // Measured, 32 query and 8 key/value heads of 128 dims: 4096 tokens 21.5 us, 4.8
-// TB/s, the rate of a large copy; one token 2.7 us in a graph, a launch.
+// TB/s, the rate of a large copy; one token 2.7 us in a graph, a launch; 2056
+// tokens of 128/8 heads of 256 dims 64-69 us, 4.4-4.8 TB/s, and 85-92 us if each
+// is of another sequence: its keys and values then go out in pieces of 16 and 2
+// bytes.  7 wavefronts a SIMD are the best number (8, with 64 registers: 69-86 us;
+// 6: 66-70 us).
 #pragma once
 
 #include "attn.hpp"
@@ -57,9 +61,23 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
   const bool turned = 8 * c < a.rotary;
   const bool apart = turned && !a.interleaved;
   const int d0 = apart ? 4 * c : 8 * c, d1 = apart ? half + 4 * c : 8 * c + 4;
+  // one piece of 16 bytes where no lane has two halves (2056 tokens of 128/8 heads
+  // of 256 dims, interleaved pairs: 64 us, and 79 us in two pieces)
+  const bool joined = a.interleaved || !a.rotary;
   const uint16_t* const x0 = a.qkv + t * a.stride;
-  uint2 raw0 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d0));
-  uint2 raw1 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(r0) * D + d1));
+  auto load_row = [&](int h, uint2& lo, uint2& hi) {
+    const uint16_t* const x = x0 + static_cast<int64_t>(h) * D;
+    if (joined) {
+      const uint4 v = load_stream(reinterpret_cast<const uint4*>(x + d0));
+      lo = uint2{v.x, v.y};
+      hi = uint2{v.z, v.w};
+    } else {
+      lo = load_stream(reinterpret_cast<const uint2*>(x + d0));
+      hi = load_stream(reinterpret_cast<const uint2*>(x + d1));
+    }
+  };
+  uint2 raw0, raw1;
+  load_row(r0, raw0, raw1);
 
   __shared__ int64_t lslot[TB];
   __shared__ __align__(16) uint16_t tile[2048];
@@ -79,10 +97,7 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
 
   for (int h = r0; h < r1; ++h) {
     const uint2 now0 = raw0, now1 = raw1;
-    if (h + 1 < r1) {
-      raw0 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d0));
-      raw1 = load_stream(reinterpret_cast<const uint2*>(x0 + static_cast<int64_t>(h + 1) * D + d1));
-    }
+    if (h + 1 < r1) load_row(h + 1, raw0, raw1);
     const bool isq = h < a.heads;
     if (h >= a.heads + a.kv_heads) {
       // values: thread (g, d) stores dim d of tokens 8 g .. 8 g + 7
@@ -155,8 +170,12 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
     if (isq) {
       if (live) {
         uint16_t* o = a.q_out + (t * a.heads + h) * D;
-        *reinterpret_cast<uint2*>(o + d0) = res0;
-        *reinterpret_cast<uint2*>(o + d1) = res1;
+        if (joined) {
+          *reinterpret_cast<uint4*>(o + d0) = uint4{res0.x, res0.y, res1.x, res1.y};
+        } else {
+          *reinterpret_cast<uint2*>(o + d0) = res0;
+          *reinterpret_cast<uint2*>(o + d1) = res1;
+        }
       }
     } else {
       // keys: thread (chunk, token) stores 16 bytes

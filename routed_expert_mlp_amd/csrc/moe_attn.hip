@@ -54,7 +54,9 @@ int validate_cache(const moe_attn_config* c, const moe_attn_cache* cache) {
   return MOE_MLP_OK;
 }
 
-constexpr int64_t PREP_BLOCKS = 1024;              // blocks of moe_attn_prepare that fill the GPU
+// Blocks of moe_attn_prepare that fill the GPU (925 tokens of 128/8 heads of 128
+// dims: 17.9 us, with 1024 blocks 19.4, with 2048 21.0).
+constexpr int64_t PREP_BLOCKS = 1536;
 
 // hipLaunchKernel says whether this launch failed; an error that an earlier
 // call of the process left behind is not taken for it.
