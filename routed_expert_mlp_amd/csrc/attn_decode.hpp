@@ -37,8 +37,9 @@ constexpr int ATTN_MAX_TPS = 64;      // most 32-key tiles of a part
 constexpr int ATTN_NW = 4;            // wavefronts of a block
 
 // Blocks that a CU holds at once, by the registers of a wavefront's sums and
-// operands (at most 256 and 512).
-constexpr int attn_blocks_per_cu(int D, int CT) { return D * CT <= 128 ? 2 : 1; }
+// operands (at most 256 and 512).  At 64 dims 4 would fit; 2, with longer parts, are
+// faster (16 sequences of 4 new tokens, window 4096: 18.4 us, and 19.9 us with 3 or 4).
+constexpr int attn_blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
 
 // Column col of a sequence and key/value head: new token col / group, head col % group.
 __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int kvh, int col) {
@@ -46,33 +47,40 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int
   return (row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
 }
 
-template <int D, int CT>
-__global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_attn_decode(AttnArgs a) {
-  constexpr int NW = ATTN_NW, KS = D / 16, DT = D / 32, COLS = 32 * CT, LD = D + 4;
+// More rows of a head than 32 (heads of the group x new tokens) take several
+// blocks, which read the same keys (AGAIN): through the caches then, around them
+// otherwise (64 sequences of up to 4096 keys, 32/8 heads of 128 dims, one token: 136
+// us around, 156 us through).  Blocks of 64 rows, which read the keys once, have
+// half as many blocks, and wavefronts, a CU: 8 sequences of 8 new tokens of 64/2
+// heads 44 us, and 35 us in blocks of 32; 64 of 4 tokens of 64/4 heads 100 and
+// 107 us, the only case of many where they were faster.
+template <int D, bool AGAIN>
+__global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_decode(AttnArgs a) {
+  constexpr int NW = ATTN_NW, KS = D / 16, DT = D / 32, COLS = 32, LD = D + 4;
   const int cols = a.n_q * a.group;
   const int col_blocks = (cols + COLS - 1) / COLS;
   // the parts of a sequence run slowest: with parts next to each other, the
   // later ones, which shorter sequences lack, would all fall to the same XCDs
   // (64 sequences of 1..8192 keys: 209 us that way, 180 us this way)
-  int bi = blockIdx.x;
+  // the column blocks that read the same keys are 8 blocks apart, on one XCD at
+  // about the same time, so that its L2 has the keys for the second (64 sequences
+  // of 4 new tokens, 64/4 heads of 256 dims, up to 4096 keys: 305 us next to each
+  // other and around the caches, 237 us this way, 211 us through the caches too)
+  const int cb = static_cast<int>(blockIdx.x / 8) % col_blocks;
+  int bi = static_cast<int>(blockIdx.x / (8 * col_blocks)) * 8 + blockIdx.x % 8;
   const int kvh = bi % a.kv_heads;
   bi /= a.kv_heads;
-  const int cb = bi % col_blocks;
-  bi /= col_blocks;
   const int b = bi % a.B, split = bi / a.B;
+  if (split >= a.splits) return;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
   const int w = uniform(tid >> 6);
   // the queries are on their way before the sequence's length is known
-  bf16x8 qf[CT][KS];
-  int pos[CT];                  // new token of this lane's columns, then its position
+  bf16x8 qf[KS];
+  const int col = min(cb * COLS + r, cols - 1);
+  const int tok = col / a.group;                   // new token of this lane's column
+  const uint16_t* qp = a.q + attn_row(a, static_cast<int64_t>(b) * a.n_q, kvh, col) * D + 8 * half;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int col = min(cb * COLS + 32 * ct + r, cols - 1);
-    pos[ct] = col / a.group;
-    const uint16_t* qp = a.q + attn_row(a, static_cast<int64_t>(b) * a.n_q, kvh, col) * D + 8 * half;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) qf[ct][ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
-  }
+  for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
   const AttnSeq s = attn_seq(a, b);
   const int first = s.len - s.n;
   AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
@@ -89,19 +97,21 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
     ids[i] = min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
   }
 
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) pos[ct] += first;
+  const int pos = first + tok;
   __syncthreads();
 
   const int ps = 1 << a.page_shift;
   const int64_t head_elems = static_cast<int64_t>(D) << a.page_shift;
+  auto load = [](const uint16_t* p) {
+    return AGAIN ? *reinterpret_cast<const uint4*>(p) : load_stream(reinterpret_cast<const uint4*>(p));
+  };
   auto load_k = [&](int v, uint4 (&kf)[KS]) {
     const int key = 32 * tl.tile(v) + swap23(r);
     const int64_t base = (static_cast<int64_t>(ids[2 * v + (r >> 4)]) * a.kv_heads + kvh) * head_elems +
                          ((half << a.page_shift) + (key & (ps - 1))) * 8;
     const uint16_t* p = a.k + base;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kf[ks] = load_stream(reinterpret_cast<const uint4*>(p + ((2 * ks * 8) << a.page_shift)));
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = load(p + ((2 * ks * 8) << a.page_shift));
   };
   auto load_v = [&](int v, uint4 (&vf)[2][DT]) {
     const int key0 = 32 * tl.tile(v);
@@ -111,21 +121,16 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
       const uint16_t* p = a.v + (static_cast<int64_t>(ids[2 * v + g]) * a.kv_heads + kvh) * head_elems +
                           at * D + r * 8;
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) vf[g][dt] = load_stream(reinterpret_cast<const uint4*>(p + 32 * 8 * dt));
+      for (int dt = 0; dt < DT; ++dt) vf[g][dt] = load(p + 32 * 8 * dt);
     }
   };
 
-  f32x16 acc[CT][DT];
-  float m[CT], l[CT];
+  f32x16 acc[DT];
+  float m = ATTN_NO_MAX, l = 0.0f;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    m[ct] = ATTN_NO_MAX;
-    l[ct] = 0.0f;
+  for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[ct][dt][e] = 0.0f;
-  }
+    for (int e = 0; e < 16; ++e) acc[dt][e] = 0.0f;
   uint4 kf[KS], vf[2][DT];
   int v = w;
   if (v < tl.n) {
@@ -133,30 +138,22 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
     load_v(v, vf);
   }
   for (; v < tl.n; v += NW) {
-    f32x16 sc[CT];
+    f32x16 sc;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sc[ct][e] = 0.0f;
+    for (int e = 0; e < 16; ++e) sc[e] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-        sc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[ks]), qf[ct][ks], sc[ct], 0, 0,
-                                                         0);
+      sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[ks]), qf[ks], sc, 0, 0, 0);
     const int vn = v + NW;
     if (vn < tl.n) load_k(vn, kf);
     const int key0 = 32 * tl.tile(v);
     // a tile that some column sees only in part: scores of invisible keys go to
     // -inf, and the values of keys that nobody sees, whatever the slots hold, to 0
     if (key0 + 31 > first || (a.window && key0 < max(0, s.len - a.window) && key0 + 31 >= tl.sinks)) {
+      const uint32_t see = static_cast<uint32_t>(
+          visible_bits(key0 + 8 * half, pos, attn_window_lo(a, pos), tl.sinks));
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const uint32_t see = static_cast<uint32_t>(
-            visible_bits(key0 + 8 * half, pos[ct], attn_window_lo(a, pos[ct]), tl.sinks));
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sc[ct][e] = keep_if(see, 16 * (e >> 3) + (e & 7), sc[ct][e]);
-      }
+      for (int e = 0; e < 16; ++e) sc[e] = keep_if(see, 16 * (e >> 3) + (e & 7), sc[e]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const uint4 mk = value_mask(static_cast<uint32_t>(
@@ -165,128 +162,101 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D, CT)) void k_att
         for (int dt = 0; dt < DT; ++dt) vf[g][dt] = and4(vf[g][dt], mk);
       }
     }
-    uint4 pf[CT][2];
+    float mx = sc[0];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      float mx = sc[ct][0];
+    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[e]);
+    const float mn = fmaxf(m, max_halves(mx) * a.scale_log2);
+    if (__any(mn > m)) {
+      const float f = exp2_fast(m - mn);
+      m = mn;
+      l *= f;
 #pragma unroll
-      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[ct][e]);
-      const float mn = fmaxf(m[ct], max_halves(mx) * a.scale_log2);
-      if (__any(mn > m[ct])) {
-        const float f = exp2_fast(m[ct] - mn);
-        m[ct] = mn;
-        l[ct] *= f;
+      for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[ct][dt][e] *= f;
-      }
-      uint32_t pk[8];
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const float p0 = exp2_fast(fmaf(sc[ct][e], a.scale_log2, -m[ct]));
-        const float p1 = exp2_fast(fmaf(sc[ct][e + 1], a.scale_log2, -m[ct]));
-        l[ct] += p0 + p1;
-        pk[e >> 1] = pack_bf16x2(p0, p1);
-      }
-      pf[ct][0] = {pk[0], pk[1], pk[2], pk[3]};
-      pf[ct][1] = {pk[4], pk[5], pk[6], pk[7]};
+        for (int e = 0; e < 16; ++e) acc[dt][e] *= f;
     }
+    uint32_t pk[8];
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float p0 = exp2_fast(fmaf(sc[e], a.scale_log2, -m));
+      const float p1 = exp2_fast(fmaf(sc[e + 1], a.scale_log2, -m));
+      l += p0 + p1;
+      pk[e >> 1] = pack_bf16x2(p0, p1);
+    }
+    const uint4 pf[2] = {{pk[0], pk[1], pk[2], pk[3]}, {pk[4], pk[5], pk[6], pk[7]}};
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          acc[ct][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g][dt]),
-                                                                __builtin_bit_cast(bf16x8, pf[ct][g]), acc[ct][dt], 0,
-                                                                0, 0);
+        acc[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[g][dt]),
+                                                          __builtin_bit_cast(bf16x8, pf[g]), acc[dt], 0, 0, 0);
     if (vn < tl.n) load_v(vn, vf);
   }
 
   // join the wavefronts: common maximum, then the sums in a tree
   const int live = min(cols - cb * COLS, COLS);
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const float lt = sum_halves(l[ct]);
-    if (half == 0) {
-      lm[w][32 * ct + r] = m[ct];
-      ll[w][32 * ct + r] = lt;
-    }
+  const float lt = sum_halves(l);
+  if (half == 0) {
+    lm[w][r] = m;
+    ll[w][r] = lt;
   }
   __syncthreads();
-  float M[CT], L[CT];
+  float M = lm[0][r], L = 0.0f;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    M[ct] = lm[0][32 * ct + r];
+  for (int i = 1; i < NW; ++i) M = fmaxf(M, lm[i][r]);
 #pragma unroll
-    for (int i = 1; i < NW; ++i) M[ct] = fmaxf(M[ct], lm[i][32 * ct + r]);
-    L[ct] = 0.0f;
+  for (int i = 0; i < NW; ++i) L += ll[i][r] * exp2_fast(lm[i][r] - M);
+  const float f = exp2_fast(m - M);
 #pragma unroll
-    for (int i = 0; i < NW; ++i) L[ct] += ll[i][32 * ct + r] * exp2_fast(lm[i][32 * ct + r] - M[ct]);
-    const float f = exp2_fast(m[ct] - M[ct]);
+  for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[ct][dt][e] *= f;
-  }
+    for (int e = 0; e < 16; ++e) acc[dt][e] *= f;
 #pragma unroll
   for (int step = NW / 2; step; step >>= 1) {
     __syncthreads();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      if (32 * ct + r < live && w >= step && w < 2 * step) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4*>(&lo_[w - step][(32 * ct + r) * LD + 32 * dt + 8 * i + 4 * half]) =
-                f32x4{acc[ct][dt][4 * i], acc[ct][dt][4 * i + 1], acc[ct][dt][4 * i + 2], acc[ct][dt][4 * i + 3]};
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      if (32 * ct + r < live && w < step) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 o = *reinterpret_cast<const f32x4*>(&lo_[w][(32 * ct + r) * LD + 32 * dt + 8 * i + 4 * half]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[ct][dt][4 * i + j] += o[j];
-          }
-      }
-    }
-  }
-  if (w != 0) return;
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    if (32 * ct + r >= live) continue;
-    const int col = cb * COLS + 32 * ct + r;
-    if (whole) {
-      const float inv = L[ct] > 0.0f ? 1.0f / L[ct] : 0.0f;
-      uint16_t* o = a.out + attn_row(a, s.row0, kvh, col) * D + 4 * half;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 p = {pack_bf16x2(acc[ct][dt][4 * i] * inv, acc[ct][dt][4 * i + 1] * inv),
-                           pack_bf16x2(acc[ct][dt][4 * i + 2] * inv, acc[ct][dt][4 * i + 3] * inv)};
-          *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
-        }
-    } else {
-      const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits + split;
-      const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
-      if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + item * 2) = float2{M[ct], L[ct]};
-      float* o = a.ws + item * D + 4 * half;
+    if (r < live && w >= step && w < 2 * step) {
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<f32x4*>(o + 32 * dt + 8 * i) =
-              f32x4{acc[ct][dt][4 * i], acc[ct][dt][4 * i + 1], acc[ct][dt][4 * i + 2], acc[ct][dt][4 * i + 3]};
+          *reinterpret_cast<f32x4*>(&lo_[w - step][r * LD + 32 * dt + 8 * i + 4 * half]) =
+              f32x4{acc[dt][4 * i], acc[dt][4 * i + 1], acc[dt][4 * i + 2], acc[dt][4 * i + 3]};
     }
+    __syncthreads();
+    if (r < live && w < step) {
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 o = *reinterpret_cast<const f32x4*>(&lo_[w][r * LD + 32 * dt + 8 * i + 4 * half]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[dt][4 * i + j] += o[j];
+        }
+    }
+  }
+  if (w != 0 || r >= live) return;
+  if (whole) {
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    uint16_t* o = a.out + attn_row(a, s.row0, kvh, col) * D + 4 * half;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 p = {pack_bf16x2(acc[dt][4 * i] * inv, acc[dt][4 * i + 1] * inv),
+                         pack_bf16x2(acc[dt][4 * i + 2] * inv, acc[dt][4 * i + 3] * inv)};
+        *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
+      }
+  } else {
+    const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits + split;
+    const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
+    if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + item * 2) = float2{M, L};
+    float* o = a.ws + item * D + 4 * half;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(o + 32 * dt + 8 * i) =
+            f32x4{acc[dt][4 * i], acc[dt][4 * i + 1], acc[dt][4 * i + 2], acc[dt][4 * i + 3]};
   }
 }
 

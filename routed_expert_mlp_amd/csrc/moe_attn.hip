@@ -93,9 +93,9 @@ int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q
 }
 
 // How a decode call is cut: columns (new tokens x query heads of a key/value
-// head) in blocks of 32 * ct, the visible tiles of 32 keys in parts.
+// head) in blocks of 32, the visible tiles of 32 keys in parts.
 struct DecodePlan {
-  int ct, col_blocks, splits, tiles_per_split;
+  int col_blocks, splits, tiles_per_split;
   int join_waves;                    // of an output row of the join
   int64_t blocks, join_blocks;
   size_t ws_bytes;
@@ -109,25 +109,18 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
     const int64_t seen = cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32);
     if (seen < tiles) tiles = seen;
   }
-  // 64 columns a block where reading the keys and values again for every 32
-  // would be more than 56 MB; below that more and smaller blocks are faster.  64
-  // columns of 128 dims, 16 key/value heads in all: 2000 keys 24.7 us, and 30.6
-  // us with 32 columns a block; 2 heads in all and 3000 keys: 13.4 and 9.9 us;
-  // 64 dims, 16 heads in all: 16000 keys 24.0 and 27.6 us, 4000 keys 17.8 and
-  // 13.8 us.  At 256 dims the sums of 64 columns would not fit the registers.
-  const int64_t again = B * c->n_kv_heads * cdiv(cols, 32) * tiles;      // tiles of 128 * head_dim bytes
-  p.ct = cols > 32 && c->head_dim != 256 && again > (int64_t(56) << 20) / (128 * c->head_dim) ? 2 : 1;
-  p.col_blocks = static_cast<int>(cdiv(cols, 32 * p.ct));
+  p.col_blocks = static_cast<int>(cdiv(cols, 32));
   // parts that together fill the places of the GPU's 256 CUs once, if all
   // sequences were as long as the longest may be; no smaller than a tile per
   // wavefront, and no larger than ATTN_MAX_TPS, since the others should not
   // wait for one long sequence
-  const int64_t places = 256 * attn_blocks_per_cu(c->head_dim, p.ct);
+  const int64_t places = 256 * attn_blocks_per_cu(c->head_dim);
   int64_t tps = cdiv(cdiv(B * c->n_kv_heads * p.col_blocks * tiles, places), ATTN_NW) * ATTN_NW;
   tps = tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
   p.tiles_per_split = static_cast<int>(tps);
   p.splits = tiles ? static_cast<int>(cdiv(tiles, tps)) : 1;
-  p.blocks = B * c->n_kv_heads * p.col_blocks * p.splits;
+  p.blocks = B * c->n_kv_heads * p.splits;
+  if (p.col_blocks > 1) p.blocks = cdiv(p.blocks, 8) * 8 * p.col_blocks;
   const int64_t rows = B * n_q * c->n_heads;
   p.join_waves = rows < 1024 ? 4 : 1;            // measured at k_attn_join
   p.join_blocks = p.splits > 1 ? cdiv(rows, 4 / p.join_waves) : 0;
@@ -205,9 +198,10 @@ int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t m
   });
 }
 
-template <int D, int CT>
+template <int D>
 int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
-  const int st = launch(k_attn_decode<D, CT>, dim3(static_cast<unsigned>(p.blocks)), dim3(ATTN_NW * 64), s, a);
+  const int st = launch(p.col_blocks > 1 ? k_attn_decode<D, true> : k_attn_decode<D, false>,
+                        dim3(static_cast<unsigned>(p.blocks)), dim3(ATTN_NW * 64), s, a);
   if (st || p.splits == 1) return st;
   const dim3 grid(static_cast<unsigned>(p.join_blocks));
   return p.join_waves == 1 ? launch(k_attn_join<D, 1>, grid, dim3(256), s, a)
@@ -258,12 +252,7 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
     const DecodePlan p = decode_plan(c, B, max_q, max_len);
     a.splits = p.splits;
     a.tiles_per_split = p.tiles_per_split;
-    return with_dim(c->head_dim, [&](auto dc) {
-      constexpr int D = decltype(dc)::value;
-      if constexpr (D != 256)
-        if (p.ct == 2) return decode<D, 2>(a, p, s);
-      return decode<D, 1>(a, p, s);
-    });
+    return with_dim(c->head_dim, [&](auto dc) { return decode<decltype(dc)::value>(a, p, s); });
   }
   return with_prefill_shape(c, T, B, max_q, max_len, [&](auto dc, auto nc) {
     constexpr int D = decltype(dc)::value, NW = decltype(nc)::value;

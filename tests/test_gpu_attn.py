@@ -108,7 +108,7 @@ def test_decode_many_rows(heads, kv, dim, new, window):
 @pytest.mark.parametrize("heads,kv,dim,new,window", [(64, 1, 128, 1, 0), (71, 1, 64, 1, 0), (16, 2, 64, 8, 9000),
                                                      (12, 1, 128, 4, 0)])
 def test_decode_wide_groups(heads, kv, dim, new, window):
-    """More than 32 rows of a key/value head over keys that are worth reading once only."""
+    """More than 32 rows of a key/value head: several blocks that read the same keys."""
     lens = [16000, 0, 5, 33, 64, 700, 1, 4001, 12, 32, 2050, 8]
     b = make_batch(config(heads, kv, dim, 64, window=window, sinks=3), lens, [new] * len(lens), seed=heads)
     print(f"[case] decode of {new * heads // kv} rows a head of {dim} dims, window {window}", flush=True)
