@@ -445,11 +445,16 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
 }
 
 // Joins the parts of the columns that k_attn_prefill left in parts: a block
-// takes 16 of a column block's columns, a wavefront four of them side by side,
-// D / 64 dims a lane, in one pass over the parts with a running maximum.
-template <int D, int NW>
+// takes 4 NC of a column block's columns, a wavefront NC of them side by side,
+// D / 64 dims a lane, in one pass over the parts with a running maximum.  Up to
+// 6400 rows a wavefront has one, and more parts in flight (50 tokens of 16/1 heads
+// of 256 dims behind 6000: 26 us in all, and 39 us with four; 400 of 16 heads,
+// 6400 rows, 46 and 49 us, of 128 dims 34.8 and 34.0 us), above that four (8 pieces
+// of 50 of 32/8 heads of 128 dims 39 us, and 43 us with one).
+template <int D, int NW, int NC>
 __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
-  constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS, ND = D / 64, PER = COLS / 16, NC = 4;
+  constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS, ND = D / 64;
+  constexpr int PER = COLS / (4 * NC), AT_ONCE = NC == 1 ? 8 : 4;
   const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads;
   int b, cb;
   if (!prefill_block<COLS>(a, bi / PER, b, cb)) return;
@@ -461,7 +466,7 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const float2* const ml = reinterpret_cast<const float2*>(a.ws + a.T * a.heads * a.splits * D);
-  const int col0 = c0 + 16 * (bi % PER) + NC * w;
+  const int col0 = c0 + 4 * NC * (bi % PER) + NC * w;
   int64_t row[NC];
   float M[NC], L[NC], o[NC][ND];
 #pragma unroll
@@ -473,7 +478,7 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
 #pragma unroll
     for (int n = 0; n < ND; ++n) o[i][n] = 0.0f;
   }
-#pragma unroll 4
+#pragma unroll AT_ONCE
   for (int j = 0; j < parts; ++j) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {

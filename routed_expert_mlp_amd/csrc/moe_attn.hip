@@ -133,6 +133,7 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
 struct PrefillPlan {
   int64_t col_blocks, tiles;         // tiles: the most that a column block can see
   int splits, tiles_per_split;
+  int join_rows;                     // of a wavefront of the join
   int64_t blocks, join_blocks;
   size_t ws_bytes;
 };
@@ -171,7 +172,8 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   p.tiles_per_split = static_cast<int>(std::max<int64_t>(size, 1));
   p.splits = tiles ? static_cast<int>(cdiv(tiles, size)) : 1;
   p.blocks = busy * p.splits;
-  p.join_blocks = p.splits > 1 ? busy * (S::COLS / 16) : 0;
+  p.join_rows = T * c->n_heads <= 6400 ? 1 : 4;       // measured at k_attn_prefill_join
+  p.join_blocks = p.splits > 1 ? busy * (S::COLS / (4 * p.join_rows)) : 0;
   if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
   return p;
 }
@@ -262,7 +264,9 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
     a.col_blocks = static_cast<int32_t>(p.col_blocks);
     const int st = launch(k_attn_prefill<D, NW>, dim3(static_cast<unsigned>(p.blocks)), dim3(NW * 64), s, a);
     if (st || p.splits == 1) return st;
-    return launch(k_attn_prefill_join<D, NW>, dim3(static_cast<unsigned>(p.join_blocks)), dim3(256), s, a);
+    const dim3 grid(static_cast<unsigned>(p.join_blocks));
+    return p.join_rows == 1 ? launch(k_attn_prefill_join<D, NW, 1>, grid, dim3(256), s, a)
+                            : launch(k_attn_prefill_join<D, NW, 4>, grid, dim3(256), s, a);
   });
 }
 
