@@ -211,6 +211,21 @@ def test_prefill(heads, kv, dim, page, new, lens, window, sinks):
     check(b, run_prefill(b, pad=2), what)
 
 
+@pytest.mark.parametrize("heads,kv,dim,new,lens,window,sinks", [
+    (32, 8, 64, [256, 3], [4000, 50], 0, 0),
+    (32, 8, 128, [300], [5000], 0, 0),
+    (32, 8, 128, [250, 1, 20], [1100, 40, 2000], 0, 0),
+    (32, 8, 256, [230, 9], [2500, 9], 0, 0),
+    (48, 4, 128, [150], [5000], 3000, 40),
+])
+def test_prefill_many_rows_in_parts(heads, kv, dim, new, lens, window, sinks):
+    """Thousands of rows far into their sequences: keys in parts, several rows a wavefront in the join."""
+    b = make_batch(config(heads, kv, dim, 32, window=window, sinks=sinks), lens, new, seed=dim + heads)
+    what = f"prefill of {sum(new) * heads} rows of {dim} dims, window {window}+{sinks}"
+    print(f"[case] {what}", flush=True)
+    check(b, run_prefill(b, pad=1), what)
+
+
 @pytest.mark.parametrize("B", [65, 200])
 def test_prefill_many_sequences(B):
     """More sequences than a wavefront has lanes, some without new tokens."""
