@@ -136,7 +136,9 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
  *   q         [T, n_heads, head_dim] bf16;  out the same shape (rows outside
  *             cu_q[0] .. cu_q[B] are not written).
  *   cu_q      [B + 1] int32, not decreasing, within 0 .. T.
- *   max_q     the most new tokens of a sequence (further ones are not computed).
+ *   max_q     the most new tokens of a sequence; further ones are not computed
+ *             (their rows of out are not written), and the first max_q keep
+ *             their positions, seq_lens[b] - (cu_q[b+1] - cu_q[b]) and on.
  */
 int moe_attn_prefill(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t T,
                      const int32_t* cu_q, int64_t B, int64_t max_q, const int32_t* seq_lens,

@@ -33,10 +33,11 @@ struct AttnArgs {
   float scale_log2;           // scale * log2(e): the softmax runs on exp2
 };
 
-// New tokens of a sequence (rows row0 .. row0 + n of q) and its length.
+// New tokens of a sequence that are computed (rows row0 .. row0 + n - 1 of q),
+// its length, and the position of row0.
 struct AttnSeq {
   int64_t row0;
-  int n, len;
+  int n, len, first;
 };
 
 // The same for every lane; said so, because values out of vector loads would
@@ -52,9 +53,11 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
     const int r1 = uniform(min(max(a.cu_q[b + 1], r0), T));
     s.row0 = r0;
     s.n = min(r1 - r0, a.n_q);
+    s.first = s.len - (r1 - r0);       // of all its new tokens, also those past n_q
   } else {
     s.row0 = static_cast<int64_t>(b) * a.n_q;
     s.n = a.n_q;
+    s.first = s.len - s.n;
   }
   return s;
 }

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
   const AttnSeq s = attn_seq(a, b);
-  const int first = s.len - s.n;
+  const int first = s.first;
   AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
   const bool whole = tl.n <= a.tiles_per_split;
   if (!tl.keep_part(split, a.tiles_per_split)) return;
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   // asked for before the sequence's length is known: whether it has that part or not
   const float2 first_ml = ml[min(lane, a.splits - 1)];
   const AttnSeq s = attn_seq(a, b);
-  const AttnTiles tl = attn_tiles<32>(a, s.len - s.n, s.len - 1);
+  const AttnTiles tl = attn_tiles<32>(a, s.first, s.len - 1);
   if (tl.n <= a.tiles_per_split) return;
   const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
   float M = ATTN_NO_MAX, L = 0.0f, o[ND] = {};

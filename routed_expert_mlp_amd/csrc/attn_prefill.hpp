@@ -133,7 +133,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   const int c0 = cb * COLS;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
   const int w = uniform(tid >> 6);
-  const int first = s.len - s.n;
+  const int first = s.first;
   const int p_first = uniform(first + c0 / a.group), p_last = uniform(first + (min(c0 + COLS, cols) - 1) / a.group);
   AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
   const bool whole = tl.n <= a.tiles_per_split;
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   int b, cb;
   if (!prefill_block<COLS>(a, bi / PER, b, cb)) return;
   const AttnSeq s = attn_seq(a, b);
-  const int cols = s.n * a.group, c0 = cb * COLS, first = s.len - s.n;
+  const int cols = s.n * a.group, c0 = cb * COLS, first = s.first;
   const AttnTiles tl = attn_tiles<TS>(a, uniform(first + c0 / a.group),
                                       uniform(first + (min(c0 + COLS, cols) - 1) / a.group));
   if (tl.n <= a.tiles_per_split) return;
