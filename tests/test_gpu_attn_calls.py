@@ -1,5 +1,6 @@
 """GPU tests of what a call of the attention operators promises beside its
 ordinary use: bounds below the lengths."""
+import pytest
 import torch
 
 from attn_util import assert_within, make_batch
