@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
   if (r1 > a.heads) {
     if (tid < TB) lslot[tid] = t0 + tid < a.T ? a.slots[t0 + tid] : -1;
   }
-  f32x4 co = {1.0f, 1.0f, 1.0f, 1.0f}, si = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 co = {}, si = {};
   if (turned && r0 < a.heads + a.kv_heads) {
     const int64_t pos = min(max(static_cast<int64_t>(a.positions[t]), int64_t(0)), a.n_positions - 1);
     const float* cs = a.cos_sin + pos * a.rotary + 4 * c;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256) void k_attn_prepare(PrepArgs a) {
         x[4 + j] = x[4 + j] * r * n1[j];
       }
     }
-    if (a.rotary) {
+    if (turned) {      // not a turn by 0: next to an infinity or a NaN that would give a NaN
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         // pair j: dims (2 j, 2 j + 1) of the lane's 8, or (j, 4 + j)

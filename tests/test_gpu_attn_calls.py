@@ -1,5 +1,5 @@
 """GPU tests of what a call of the attention operators promises beside its
-ordinary use: bounds below the lengths."""
+ordinary use: bounds below the lengths, values that are not finite."""
 import pytest
 import torch
 
@@ -34,3 +34,34 @@ def test_prefill_of_more_new_tokens_than_max_q(heads, kv, dim, new, lens, max_q,
         n = min(max_q, new[i])
         assert_within(got[cu[i]:cu[i] + n], want[:n], bound[:n], f"{what}, sequence {i}")
         assert (got[cu[i] + n:cu[i + 1]] == 7.0).all(), f"{what}, sequence {i}: a row past max_q was written"
+
+
+@pytest.mark.parametrize("style", [A.ROPE_HALF, A.ROPE_INTERLEAVED])
+@pytest.mark.parametrize("dim,rotary", [(64, 16), (128, 64), (256, 0), (256, 128)])
+def test_prepare_passes_dims_past_the_rotation_through(dim, rotary, style):
+    """Without a norm, dims that are not rotated go out as they came in, whatever they are: infinities, NaN and
+    negative zeros stay in their own places."""
+    T, heads, kv, page = 21, 4, 2, 16
+    cfg = config(heads, kv, dim, page, rotary=rotary, style=style)
+    print(f"[case] prepare, {dim} dims of which {rotary} are rotated, style {style}, values not finite", flush=True)
+    g = torch.Generator().manual_seed(dim + rotary)
+    x = torch.randn((T, heads + 2 * kv, dim), generator=g).to(torch.bfloat16)
+    for i, odd in enumerate((float("inf"), -float("inf"), float("nan"), -0.0)):
+        at = torch.randint(rotary, dim, (T, heads + kv), generator=g)
+        keep = torch.rand((T, heads + kv), generator=g) < 0.7
+        for t, h in keep.nonzero().tolist():
+            x[t, h, at[t, h]] = odd
+    qkv = x.reshape(T, -1).to(DEV)
+    k, v = (torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in A.cache_shapes(cfg, 2))
+    q = torch.zeros((T, heads, dim), dtype=torch.bfloat16, device=DEV)
+    angle = torch.randn((32, max(rotary // 2, 1)), generator=g)
+    table = torch.cat([angle.cos(), angle.sin()], dim=1)[:, :rotary].contiguous().to(DEV) if rotary else None
+    positions = torch.arange(T, dtype=torch.int32, device=DEV) if rotary else None
+    A.moe_attn_prepare(cfg, A.KVCache(k, v), qkv, None, None, table, positions, torch.arange(T, device=DEV), q)
+    keys = k.permute(0, 3, 1, 2, 4).reshape(-1, kv, dim)[:T]
+    for got, want in ((q.cpu(), x[:, :heads]), (keys.cpu(), x[:, heads:heads + kv])):
+        assert torch.isfinite(got[..., :rotary].float()).all(), "a value that is not rotated reached the rotated dims"
+        got, want = got[..., rotary:].contiguous(), want[..., rotary:].contiguous()
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
