@@ -102,9 +102,11 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
  * Workspace bytes of moe_attn_decode (prefill == 0; max_q = its n_q) or
  * moe_attn_prefill (prefill != 0) for T new tokens (decode: B * n_q) of B
  * sequences of at most max_q new tokens and at most max_len tokens in all.
- * `bytes` is a HOST pointer.  MOE_MLP_ERR_BAD_SHAPE also for sizes whose launch
- * would have 2^32 threads or more (tens of thousands of sequences that may all
- * be very long).
+ * `bytes` is a HOST pointer.  Limits (MOE_MLP_ERR_BAD_SHAPE past them, here and
+ * in the calls): max_len < 2^30; decode: B * n_q * n_heads < 2^26; prefill:
+ * T < 2^26, min(max_q, T) * n_heads < 2^30, and B < 2^16 or
+ * B * max_q * n_heads < 2^26; and no launch of 2^32 threads or more (tens of
+ * thousands of sequences that may all be very long).
  */
 int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
                             int prefill, size_t* bytes);

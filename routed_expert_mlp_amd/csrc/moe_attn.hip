@@ -21,6 +21,8 @@ using namespace moe;
 
 constexpr int64_t kInt32End = int64_t(1) << 31;
 constexpr int64_t kMaxTokens = int64_t(1) << 26;   // rows of one call
+constexpr int64_t kMaxColumns = int64_t(1) << 30;  // prefill: heads of a sequence's rows, which the kernels count in 32 bits
+constexpr int64_t kMaxRagged = int64_t(1) << 16;   // prefill: sequences that each wavefront goes through to find its own
 constexpr int64_t kMaxKeys = int64_t(1) << 30;     // no sequence is as long: as good as no limit
 constexpr int64_t kMaxThreads = int64_t(1) << 32;  // of a launch, along one side; a grid takes fewer
 
@@ -88,7 +90,8 @@ int validate_sizes(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q
   if (B < 0 || max_q < 0 || max_len < 0 || B >= kInt32End || max_q >= kInt32End || max_len >= kMaxKeys)
     return MOE_MLP_ERR_BAD_SHAPE;
   if (!prefill && (max_q < 1 || max_q > MOE_ATTN_DECODE_MAX_Q)) return MOE_MLP_ERR_BAD_SHAPE;
-  if (B && max_q * c->n_heads >= kMaxTokens / B) return MOE_MLP_ERR_BAD_SHAPE;
+  if (B && max_q * c->n_heads >= kMaxTokens / B && (!prefill || B >= kMaxRagged)) return MOE_MLP_ERR_BAD_SHAPE;
+  if (B && prefill && std::min(max_q, T) * c->n_heads >= kMaxColumns) return MOE_MLP_ERR_BAD_SHAPE;
   return MOE_MLP_OK;
 }
 
@@ -142,6 +145,7 @@ template <int D, int NW>
 PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len) {
   using S = PrefillShape<D, NW>;
   PrefillPlan p{};
+  max_q = std::min(max_q, T);
   const int64_t group = c->n_heads / c->n_kv_heads;
   // every sequence leaves at most one column block unfilled
   p.col_blocks = std::min(B * cdiv(max_q * group, S::COLS), T * group / S::COLS + B);

@@ -184,3 +184,24 @@ def test_workspace_size_and_refusal():
     c = cfg()
     assert A._lib().moe_attn_workspace_size(ctypes.byref(c), 1, 1, 1, 16, 0, None) == capi.ERR_NULL_ARG
     assert n.value == 0
+
+
+def test_ragged_prefill_is_limited_by_its_tokens():
+    """Many sequences of which one has a long piece: what counts is the tokens, not sequences times the longest."""
+    c = cfg(n_heads=32, n_kv_heads=8)
+    assert size(c, B=256, max_q=8192, max_len=16384, prefill=1, T=8447)[0] == capi.OK
+    assert size(c, B=64, max_q=32768, max_len=65536, prefill=1, T=32768 + 63)[0] == capi.OK
+    assert size(c, B=(1 << 16) - 1, max_q=1 << 20, max_len=1 << 21, prefill=1, T=1 << 20)[0] == capi.OK
+    assert size(c, B=1 << 16, max_q=64, max_len=64, prefill=1, T=1 << 16)[0] == capi.ERR_BAD_SHAPE
+    # a bound above the tokens counts as the tokens
+    assert size(c, B=1, max_q=(1 << 31) - 1, max_len=64, prefill=1, T=64) == (capi.OK, 0)
+    for dim in (64, 128, 256):
+        wide = cfg(n_heads=64, n_kv_heads=1, head_dim=dim)
+        assert size(wide, B=1, max_q=(1 << 24) - 1, max_len=1 << 24, prefill=1, T=(1 << 24) - 1)[0] == capi.OK
+        assert size(wide, B=1, max_q=1 << 24, max_len=1 << 24, prefill=1, T=1 << 24)[0] == capi.ERR_BAD_SHAPE
+    wide = cfg(n_heads=1024, n_kv_heads=1024, head_dim=256)
+    for B in (1, (1 << 16) - 1, (1 << 31) - 1):
+        for max_q in (1, 1 << 10, (1 << 31) - 1):
+            st = size(wide, B=B, max_q=max_q, max_len=(1 << 30) - 1, prefill=1, T=(1 << 26) - 1)[0]
+            assert st == (capi.OK if B * max_q <= 1 << 10 else capi.ERR_BAD_SHAPE)
+    assert prefill(c, cache(), B=256, max_q=1 << 20, T=8447, wsb=0, q=None) == capi.ERR_NULL_ARG

@@ -1,11 +1,12 @@
 """GPU tests of what a call of the attention operators promises beside its
-ordinary use: bounds below the lengths, values that are not finite."""
+ordinary use: bounds below the lengths, values that are not finite, batches far
+more ragged than usual."""
 import pytest
 import torch
 
 from attn_util import assert_within, make_batch
 from routed_expert_mlp_amd import attention as A
-from test_gpu_attn import DEV, cache_of, config
+from test_gpu_attn import DEV, cache_of, config, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,21 @@ def test_prepare_passes_dims_past_the_rotation_through(dim, rotary, style):
         nan = torch.isnan(want)
         assert torch.equal(torch.isnan(got), nan)
         assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
+
+
+def test_prefill_of_one_long_piece_among_thousands_of_sequences():
+    """Sequences times the longest piece is past what a call may have of tokens; the tokens themselves are few."""
+    B, long = 8192, 1024
+    new = [1 if b % 3 else 0 for b in range(B)]
+    new[5000] = long
+    lens = [n + b % 5 for b, n in enumerate(new)]
+    b = make_batch(config(8, 2, 64, 16), lens, new, seed=22)
+    print(f"[case] prefill of {sum(new)} tokens of {B} sequences, one of {long}", flush=True)
+    got, row = run_prefill(b).double().cpu().numpy(), 0
+    worst = 0.0
+    for want, bound in b.expected():
+        err = abs(got[row:row + want.shape[0]] - want)
+        assert (err <= bound).all(), f"row {row} and on"
+        worst = max(worst, float((err / bound.clip(min=1e-300)).max(initial=0.0)))
+        row += want.shape[0]
+    print(f"[parity] prefill, one long piece among {B} sequences: worst error {worst:.3f} of its bound", flush=True)
