@@ -335,6 +335,8 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, in
   const int st = validate_sizes(cfg, T, B, max_q, max_len, prefill);
   if (st) return st;
   if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = 0;
+  if (B == 0 || (prefill && (T == 0 || max_q == 0))) return MOE_MLP_OK;   // nothing to do
   if (!prefill) {
     const DecodePlan p = decode_plan(cfg, B, max_q, max_len);
     if (p.blocks >= kMaxThreads / (ATTN_NW * 64) || p.join_blocks >= kMaxThreads / 256)

@@ -205,3 +205,15 @@ def test_ragged_prefill_is_limited_by_its_tokens():
             st = size(wide, B=B, max_q=max_q, max_len=(1 << 30) - 1, prefill=1, T=(1 << 26) - 1)[0]
             assert st == (capi.OK if B * max_q <= 1 << 10 else capi.ERR_BAD_SHAPE)
     assert prefill(c, cache(), B=256, max_q=1 << 20, T=8447, wsb=0, q=None) == capi.ERR_NULL_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(B=0), dict(max_q=0), dict(T=0)])
+def test_nothing_to_do_needs_no_workspace(kw):
+    c = cfg(n_heads=32, n_kv_heads=8)
+    assert size(c, prefill=1, **{**dict(B=1, max_q=4096, max_len=1 << 20, T=4096), **kw}) == (capi.OK, 0)
+    for dim in (64, 128, 256):
+        c = cfg(n_heads=1024, n_kv_heads=1024, head_dim=dim)
+        most = dict(B=1, max_q=1, max_len=(1 << 30) - 1, T=(1 << 26) - 1)
+        assert size(c, prefill=1, **{**most, **kw}) == (capi.OK, 0)
+    if "B" in kw:
+        assert size(c, prefill=0, B=0, max_q=8, max_len=(1 << 30) - 1, T=0) == (capi.OK, 0)
