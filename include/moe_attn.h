@@ -107,9 +107,19 @@ int moe_attn_prepare(const moe_attn_config* cfg, const moe_attn_cache* cache, co
  * T < 2^26, min(max_q, T) * n_heads < 2^30, and B < 2^16 or
  * B * max_q * n_heads < 2^26; and no launch of 2^32 threads or more (tens of
  * thousands of sequences that may all be very long).
+ * The size holds for these arguments alone: a call of fewer or shorter sequences
+ * may be cut into more parts, and need more.
  */
 int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
                             int prefill, size_t* bytes);
+
+/*
+ * Bytes that are enough for every call of this configuration (and of this form,
+ * decode or prefill) with none of T, B, max_q and max_len larger: for a workspace
+ * that is allocated once.  Errors as above, for these sizes.
+ */
+int moe_attn_workspace_bound(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
+                             int prefill, size_t* bytes);
 
 /*
  * Attention of n_q new tokens (1..MOE_ATTN_DECODE_MAX_Q: one, or a verify

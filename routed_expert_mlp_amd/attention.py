@@ -27,7 +27,8 @@ ROPE_INTERLEAVED = 1
 MAX_HEADS = 1024
 DECODE_MAX_Q = 8
 
-EXPORTED = ("moe_attn_prepare", "moe_attn_workspace_size", "moe_attn_decode", "moe_attn_prefill")
+EXPORTED = ("moe_attn_prepare", "moe_attn_workspace_size", "moe_attn_workspace_bound", "moe_attn_decode",
+            "moe_attn_prefill")
 
 
 class moe_attn_config(ctypes.Structure):
@@ -52,6 +53,7 @@ def _lib() -> ctypes.CDLL:
         cfgp, cp = ctypes.POINTER(moe_attn_config), ctypes.POINTER(moe_attn_cache)
         L.moe_attn_prepare.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp]
         L.moe_attn_workspace_size.argtypes = [cfgp, i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(sz)]
+        L.moe_attn_workspace_bound.argtypes = L.moe_attn_workspace_size.argtypes
         L.moe_attn_decode.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         L.moe_attn_prefill.argtypes = [cfgp, cp, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         for n in EXPORTED:
@@ -108,10 +110,20 @@ def new_cache(cfg: AttnConfig, n_pages: int, device="cuda") -> KVCache:
 
 
 def moe_attn_workspace_size(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill: bool) -> int:
-    """Bytes for T new tokens of B sequences, at most max_q of one, each of at most max_len tokens in all."""
+    """Bytes for T new tokens of B sequences, at most max_q of one, each of at most max_len tokens in all; of exactly
+    these sizes, since smaller ones may need more (moe_attn_workspace_bound)."""
+    return _size("moe_attn_workspace_size", cfg, T, B, max_q, max_len, prefill)
+
+
+def moe_attn_workspace_bound(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill: bool) -> int:
+    """Bytes for every call of these sizes or smaller ones: for a workspace that is allocated once."""
+    return _size("moe_attn_workspace_bound", cfg, T, B, max_q, max_len, prefill)
+
+
+def _size(name, cfg, T, B, max_q, max_len, prefill) -> int:
     n = ctypes.c_size_t(0)
-    _check(_lib().moe_attn_workspace_size(ctypes.byref(cfg.c()), int(T), int(B), int(max_q), int(max_len),
-                                          int(bool(prefill)), ctypes.byref(n)), "moe_attn_workspace_size")
+    _check(getattr(_lib(), name)(ctypes.byref(cfg.c()), int(T), int(B), int(max_q), int(max_len),
+                                 int(bool(prefill)), ctypes.byref(n)), name)
     return n.value
 
 

@@ -30,6 +30,7 @@ struct AttnArgs {
   int32_t window, sinks;      // window 0: none
   int32_t splits, tiles_per_split;   // parts of the visible tiles (at most), and their size
   int32_t col_blocks;         // prefill: column blocks of all sequences (at most)
+  int32_t ws_cols;            // prefill: columns that a block has in the workspace
   float scale_log2;           // scale * log2(e): the softmax runs on exp2
 };
 

@@ -105,6 +105,16 @@ __device__ __forceinline__ int scalar(int v) {
   return v;
 }
 
+// Where a column of a block (column block `block` of all, as prefill_block counts
+// them) has its parts in the workspace: their sums, and behind all sums their
+// maxima and totals.  By blocks and not by rows of q, so that the room that parts
+// need follows the places of the GPU and not T.
+__device__ __forceinline__ int64_t prefill_item(const AttnArgs& a, int block, int kvh, int col) {
+  return ((static_cast<int64_t>(block) * a.kv_heads + kvh) * a.ws_cols + col) * a.splits;
+}
+
+__device__ __forceinline__ int64_t prefill_items(const AttnArgs& a) { return prefill_item(a, a.col_blocks, 0, 0); }
+
 // Weights may exceed the running maximum by this many powers of two before
 // the sums are rescaled (fp32 sums and bf16 weights have the range).
 constexpr float PF_SLACK = 8.0f;
@@ -421,7 +431,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   if (c0 + 32 * w + r >= cols) return;
   const int64_t row = row_of();
   if (!whole) {
-    const int64_t item = row * a.splits + split, items = a.T * a.heads * a.splits;
+    const int64_t item = prefill_item(a, bi - split * a.col_blocks, kvh, 32 * w + r) + split, items = prefill_items(a);
     if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + 2 * item) = float2{m, lt};
     float* o = a.ws + item * D + 4 * half;
 #pragma unroll
@@ -465,14 +475,15 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   if (tl.n <= a.tiles_per_split) return;
   const int parts = (tl.n + a.tiles_per_split - 1) / a.tiles_per_split;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-  const float2* const ml = reinterpret_cast<const float2*>(a.ws + a.T * a.heads * a.splits * D);
+  const float2* const ml = reinterpret_cast<const float2*>(a.ws + prefill_items(a) * D);
   const int col0 = c0 + 4 * NC * (bi % PER) + NC * w;
-  int64_t row[NC];
+  int64_t row[NC], first_item[NC];
   float M[NC], L[NC], o[NC][ND];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int col = min(col0 + i, cols - 1), t = col / a.group;
     row[i] = (s.row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
+    first_item[i] = prefill_item(a, bi / PER, kvh, col - c0);
     M[i] = ATTN_NO_MAX;
     L[i] = 0.0f;
 #pragma unroll
@@ -482,7 +493,7 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(AttnArgs a) {
   for (int j = 0; j < parts; ++j) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int64_t item = row[i] * a.splits + j;
+      const int64_t item = first_item[i] + j;
       const float2 p = ml[item];
       const float* src = a.ws + item * D + lane * ND;
       const float mn = fmaxf(M[i], p.x);

@@ -104,14 +104,17 @@ struct DecodePlan {
   size_t ws_bytes;
 };
 
+// The most 32-key tiles that the new tokens of a sequence see.
+int64_t decode_tiles(const moe_attn_config* c, int64_t n_q, int64_t max_len) {
+  const int64_t tiles = cdiv(max_len, 32);
+  if (!c->window) return tiles;
+  return std::min(tiles, cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32));
+}
+
 DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len) {
   DecodePlan p{};
   const int64_t cols = n_q * (c->n_heads / c->n_kv_heads);
-  int64_t tiles = cdiv(max_len, 32);
-  if (c->window) {
-    const int64_t seen = cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(c->n_sinks, 32);
-    if (seen < tiles) tiles = seen;
-  }
+  const int64_t tiles = decode_tiles(c, n_q, max_len);
   p.col_blocks = static_cast<int>(cdiv(cols, 32));
   // parts that together fill the places of the GPU's 256 CUs once, if all
   // sequences were as long as the longest may be; no smaller than a tile per
@@ -131,15 +134,32 @@ DecodePlan decode_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   return p;
 }
 
+// The most workspace of a decode call with no larger sizes.  Items (a column's
+// sums of a part) are rows x parts.  Parts shorter than ATTN_MAX_TPS are at most
+// places / blocks + 1 of each sequence, and a block has at most min(cols, 32)
+// columns; the others are as many as the longest sequence has.
+size_t decode_bound(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len) {
+  const int64_t tiles = decode_tiles(c, n_q, max_len);
+  if (tiles <= ATTN_NW) return 0;
+  const int64_t cols = n_q * (c->n_heads / c->n_kv_heads), rows = B * c->n_kv_heads * cols;
+  int64_t items = std::min(rows * cdiv(tiles, ATTN_NW),
+                           std::min<int64_t>(cols, 32) * 256 * attn_blocks_per_cu(c->head_dim) + rows);
+  if (tiles > ATTN_MAX_TPS) items = std::max(items, rows * cdiv(tiles, ATTN_MAX_TPS));
+  return size_t(items) * (c->head_dim + 2) * 4;
+}
+
 // How a prefill call is cut: column blocks of all sequences, and the visible tiles of a
 // block in parts where there are too few blocks to fill the GPU.
 struct PrefillPlan {
   int64_t col_blocks, tiles;         // tiles: the most that a column block can see
   int splits, tiles_per_split;
+  int ws_cols;                       // columns of a block that can be there
   int join_rows;                     // of a wavefront of the join
   int64_t blocks, join_blocks;
-  size_t ws_bytes;
+  size_t ws_bytes, ws_bound;
 };
+
+constexpr int64_t PF_LEAST = 8;      // tiles of a part, but for a last one
 
 template <int D, int NW>
 PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len) {
@@ -157,28 +177,34 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   // join: about TILE_NS a tile, 1.6 times that with two blocks on a CU, and for
   // the join 4 us and the partial sums' way out and back.  Parts of one size that
   // have places at once, or as many as there are places if all blocks were as
-  // long as the longest may be; none shorter than 8 tiles.  32/8 heads: 512
+  // long as the longest may be; none shorter than PF_LEAST tiles.  32/8 heads: 512
   // tokens behind 65024 cached ones 473 us, and 1255 us whole; 64 behind 7168
   // 25 and 141 us, behind 1024 14.5 and 23 us; 8 pieces of 8/2 heads of 256 dims
   // behind prefixes (178 blocks at most) 82 and 116 us; but 1024 tokens of a
   // prompt 23.4 us whole, and 28.8 us in two parts.
   constexpr int64_t TILE_NS = D == 64 ? 600 : D == 256 ? 780 : NW == 8 ? 1900 : 550;
-  const int64_t places = 256 * S::PER_CU;
+  const int64_t places = 256 * S::PER_CU, rows = std::min(T, B * max_q) * c->n_heads;
   int64_t size = tiles, best = tiles * TILE_NS * (busy > 256 ? 8 : 5) / 5;
   auto consider = [&](int64_t tps) {
     const int64_t ns = tps * TILE_NS * (busy * tiles > 256 * tps ? 8 : 5) / 5 + 4000 +
-                       T * c->n_heads * cdiv(tiles, tps) * D * 8 / (D == 64 ? 4000 : 6000);
+                       rows * cdiv(tiles, tps) * D * 8 / (D == 64 ? 4000 : 6000);
     if (ns < best) best = ns, size = tps;
   };
-  for (int64_t n = 2; busy * n <= places && tiles >= 8 * n; n += n / 4 + 1) consider(cdiv(tiles, n));
-  if (busy <= places) consider(std::max<int64_t>(cdiv(busy * tiles, places), 8));
+  for (int64_t n = 2; busy * n <= places && tiles >= PF_LEAST * n; n += n / 4 + 1) consider(cdiv(tiles, n));
+  if (busy <= places) consider(std::max(cdiv(busy * tiles, places), PF_LEAST));
   p.tiles = tiles;
   p.tiles_per_split = static_cast<int>(std::max<int64_t>(size, 1));
   p.splits = tiles ? static_cast<int>(cdiv(tiles, size)) : 1;
   p.blocks = busy * p.splits;
-  p.join_rows = T * c->n_heads <= 6400 ? 1 : 4;       // measured at k_attn_prefill_join
+  p.join_rows = rows <= 6400 ? 1 : 4;                 // measured at k_attn_prefill_join
   p.join_blocks = p.splits > 1 ? busy * (S::COLS / (4 * p.join_rows)) : 0;
-  if (p.splits > 1) p.ws_bytes = size_t(T) * c->n_heads * p.splits * (D + 2) * 4;
+  p.ws_cols = static_cast<int>(std::min<int64_t>(max_q * group, S::COLS));
+  if (p.splits > 1) p.ws_bytes = size_t(p.blocks) * p.ws_cols * (D + 2) * 4;
+  // The most that a call with no larger sizes takes: parts come only where the
+  // column blocks have places at once, at most ceil(places / blocks) of each, none
+  // shorter than PF_LEAST tiles.
+  if (tiles > PF_LEAST)
+    p.ws_bound = size_t(std::min(busy * cdiv(tiles, PF_LEAST), places + std::min(busy, places))) * p.ws_cols * (D + 2) * 4;
   return p;
 }
 
@@ -266,6 +292,7 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
     a.splits = p.splits;
     a.tiles_per_split = p.tiles_per_split;
     a.col_blocks = static_cast<int32_t>(p.col_blocks);
+    a.ws_cols = p.ws_cols;
     const int st = launch(k_attn_prefill<D, NW>, dim3(static_cast<unsigned>(p.blocks)), dim3(NW * 64), s, a);
     if (st || p.splits == 1) return st;
     const dim3 grid(static_cast<unsigned>(p.join_blocks));
@@ -350,6 +377,27 @@ int moe_attn_workspace_size(const moe_attn_config* cfg, int64_t T, int64_t B, in
     if (p.col_blocks >= kInt32End || p.blocks >= kMaxThreads / (NW * 64) || p.join_blocks >= kMaxThreads / 256)
       return MOE_MLP_ERR_BAD_SHAPE;
     *bytes = p.ws_bytes;
+    return MOE_MLP_OK;
+  });
+}
+
+int moe_attn_workspace_bound(const moe_attn_config* cfg, int64_t T, int64_t B, int64_t max_q, int64_t max_len,
+                             int prefill, size_t* bytes) {
+  size_t need = 0;
+  const int st = moe_attn_workspace_size(cfg, T, B, max_q, max_len, prefill, &need);
+  if (st) return st;
+  if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = 0;
+  if (B == 0 || (prefill && (T == 0 || max_q == 0))) return MOE_MLP_OK;
+  if (!prefill) {
+    *bytes = decode_bound(cfg, B, max_q, max_len);
+    return MOE_MLP_OK;
+  }
+  // smaller calls may take either number of wavefronts
+  return with_dim(cfg->head_dim, [&](auto dc) -> int {
+    constexpr int D = decltype(dc)::value;
+    *bytes = prefill_plan<D, 4>(cfg, T, B, max_q, max_len).ws_bound;
+    if constexpr (D == 128) *bytes = std::max(*bytes, prefill_plan<D, 8>(cfg, T, B, max_q, max_len).ws_bound);
     return MOE_MLP_OK;
   });
 }

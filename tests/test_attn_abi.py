@@ -4,6 +4,7 @@ enqueued (so fake device addresses are safe)."""
 import ctypes
 import math
 import os
+import random
 import re
 
 import pytest
@@ -217,3 +218,66 @@ def test_nothing_to_do_needs_no_workspace(kw):
         assert size(c, prefill=1, **{**most, **kw}) == (capi.OK, 0)
     if "B" in kw:
         assert size(c, prefill=0, B=0, max_q=8, max_len=(1 << 30) - 1, T=0) == (capi.OK, 0)
+
+
+def bound(c, B, max_q, max_len, prefill, T):
+    n = ctypes.c_size_t(0)
+    st = A._lib().moe_attn_workspace_bound(ctypes.byref(c) if c is not None else None, T, B, max_q, max_len, prefill,
+                                           ctypes.byref(n))
+    return st, n.value
+
+
+GEOMETRIES = [dict(n_heads=h, n_kv_heads=k, head_dim=d, window=w, n_sinks=s)
+              for h, k in ((32, 8), (64, 2), (8, 8), (71, 1)) for d in (64, 128, 256) for w, s in ((0, 0), (3000, 70))]
+
+
+@pytest.mark.parametrize("pf", [0, 1])
+@pytest.mark.parametrize("kw", GEOMETRIES, ids=lambda kw: "-".join(str(v) for v in kw.values()))
+def test_workspace_bound_covers_every_smaller_call(kw, pf):
+    """The bound of some largest sizes is at least the size, and the bound, of smaller ones, and no call within it
+    is refused for its workspace."""
+    rng, c = random.Random(f"{kw} {pf}"), cfg(**kw)
+
+    def any_up_to(n):
+        return rng.choice([n, rng.randint(1, n), max(1, int(math.exp(rng.uniform(0, math.log(n)))))])
+
+    parts = 0
+    for _ in range(12):
+        B, max_q = any_up_to(200), any_up_to(8192 if pf else 8)
+        max_len = any_up_to(200000)
+        T = rng.choice([B * max_q, any_up_to(B * max_q), 3 * B * max_q]) if pf else B * max_q
+        st, most = bound(c, B, max_q, max_len, pf, T)
+        assert st == capi.OK
+        for _ in range(300):
+            b, q, n = any_up_to(B), any_up_to(max_q), any_up_to(max_len)
+            t = any_up_to(T) if pf else b * q
+            st, need = size(c, B=b, max_q=q, max_len=n, prefill=pf, T=t)
+            st2, less = bound(c, b, q, n, pf, t)
+            assert st == st2 == capi.OK and need <= less <= most, (B, max_q, max_len, T, b, q, n, t)
+            parts += need > 0
+    assert parts > 100
+
+
+def test_workspace_of_parts_follows_the_gpu_and_not_the_rows():
+    """Rows of q that belong to no sequence take no room, and the bound of prefill stays below 70 MB."""
+    c = cfg(n_heads=32, n_kv_heads=8)
+    small = size(c, B=1, max_q=1, max_len=65536, prefill=1, T=1)
+    assert small[0] == capi.OK and 0 < small[1] < 2 << 20
+    assert size(c, B=1, max_q=1, max_len=65536, prefill=1, T=100000) == small
+    for kw in GEOMETRIES:
+        assert 0 < bound(cfg(**kw), 1000, 100000, 1 << 20, 1, 1 << 20)[1] < 70 << 20
+    # a call of a tile's length is one part whatever its batch
+    assert bound(c, 1000, 8, 128, 0, 8000) == (capi.OK, 0)
+
+
+def test_workspace_bound_refuses_what_the_size_does():
+    assert bound(None, 1, 1, 64, 0, 1)[0] == capi.ERR_NULL_ARG
+    assert bound(cfg(head_dim=96), 1, 1, 64, 1, 1)[0] == capi.ERR_BAD_SHAPE
+    for pf in (0, 1):
+        for kw in (dict(B=-1), dict(max_q=-1), dict(max_len=-1), dict(T=-1), dict(max_len=1 << 62), dict(B=1 << 62),
+                   dict(T=1 << 62)):
+            assert bound(cfg(), **{**dict(B=2, max_q=4, max_len=64, prefill=pf, T=8), **kw})[0] == capi.ERR_BAD_SHAPE
+    assert bound(cfg(), 0, 8, 1 << 29, 1, 1000) == (capi.OK, 0)
+    assert bound(cfg(), 0, 8, 1 << 29, 0, 0) == (capi.OK, 0)
+    c = cfg()
+    assert A._lib().moe_attn_workspace_bound(ctypes.byref(c), 1, 1, 1, 16, 0, None) == capi.ERR_NULL_ARG

@@ -1,12 +1,12 @@
 """GPU tests of what a call of the attention operators promises beside its
 ordinary use: bounds below the lengths, values that are not finite, batches far
-more ragged than usual."""
+more ragged than usual, one workspace for calls of many sizes."""
 import pytest
 import torch
 
 from attn_util import assert_within, make_batch
 from routed_expert_mlp_amd import attention as A
-from test_gpu_attn import DEV, cache_of, config, run_prefill
+from test_gpu_attn import DEV, cache_of, check, config, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,34 @@ def test_prefill_of_one_long_piece_among_thousands_of_sequences():
         worst = max(worst, float((err / bound.clip(min=1e-300)).max(initial=0.0)))
         row += want.shape[0]
     print(f"[parity] prefill, one long piece among {B} sequences: worst error {worst:.3f} of its bound", flush=True)
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(32, 8, 128), (8, 2, 64), (16, 2, 256)])
+def test_one_workspace_for_calls_of_many_sizes(heads, kv, dim):
+    """A workspace of the bound of the largest sizes serves smaller calls, whether in parts or whole; what lies behind
+    the bytes that a call asks for stays as it was."""
+    cfg = config(heads, kv, dim, 32)
+    B, max_q, max_len = 4, 600, 6000
+    most = [A.moe_attn_workspace_bound(cfg, B * max_q, B, max_q, max_len, True),
+            A.moe_attn_workspace_bound(cfg, B * 4, B, 4, max_len, False)]
+    ws = torch.full((max(most),), 255, dtype=torch.uint8, device=DEV)      # NaN in every float
+    for new, lens in (([1], [6000]), ([7], [5000]), ([90], [3000]), ([20, 0, 3], [2500, 10, 40]), ([200], [200]),
+                      ([4, 4, 4, 4], [6000, 3, 900, 4]), ([2, 2], [30, 6000])):
+        b = make_batch(cfg, lens, new, seed=dim + sum(lens))
+        q, table = b.q.to(DEV), b.table.to(DEV)
+        n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        cu = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32, device=DEV)
+        for form in ("prefill", "decode"):
+            if form == "decode" and (len(set(new)) > 1 or new[0] > 4):
+                continue
+            need = A.moe_attn_workspace_size(cfg, sum(new), len(new), max(new), max(lens), form == "prefill")
+            print(f"[case] {form} of {new} behind {lens}, {heads}/{kv}x{dim}: {need} bytes of {ws.numel()}", flush=True)
+            out = torch.full_like(q, float("nan"))
+            ws.fill_(255)
+            if form == "prefill":
+                A.moe_attn_prefill(cfg, cache_of(b), q, cu, max(new), n, table, max(lens), out, ws)
+            else:
+                shape = (len(new), new[0], heads, dim)
+                A.moe_attn_decode(cfg, cache_of(b), q.view(shape), n, table, max(lens), out.view(shape), ws)
+            assert torch.all(ws[need:] == 255), "the call wrote behind the bytes that it asks for"
+            check(b, out, f"{form} with one workspace")
