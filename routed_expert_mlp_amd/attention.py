@@ -9,7 +9,11 @@ pointers and torch's current HIP stream, and raises MoeMlpError on a non-zero
 status; the library does all of the computing.
 
 bind_prepare, bind_decode and bind_prefill check and marshal once and return a
-callable that issues the call again on the same buffers (serving loops).
+callable that issues the call again on the same buffers (serving loops).  It
+goes to the stream given when binding; with none given, to torch's current
+stream of the buffers' device at the time of each call, so that it can be
+called, or captured, under another stream than it was bound under.  Calls of one
+callable share its workspace: two of them must not run at the same time.
 """
 from __future__ import annotations
 
@@ -150,11 +154,22 @@ def _ws_on_stream(cfg, T, B, max_q, max_len, prefill, device, stream) -> torch.T
         return workspace(cfg, T, B, max_q, max_len, prefill, device)
 
 
-def _callable(name: str, args, keep):
+def _callable(name: str, args, stream, device: int, keep, ws: Optional[torch.Tensor] = None):
+    """args: all but the stream; ws: the workspace if it is the callable's own, allocated on the stream current now."""
     fn = getattr(_lib(), name)
+    # looked up and converted once: a call of the smallest sizes is bound by what it does on the host
+    handle_of, device_now = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    args = tuple(to(a) if a is None or isinstance(a, int) else a for to, a in zip(fn.argtypes, args))
+    fixed = None if stream is None else _stream(stream)
+    home = handle_of(device)
 
     def call():
-        st = fn(*args)
+        if device_now() != device:
+            raise ValueError(f"{name}: bound on cuda:{device}, the current device is cuda:{device_now()}")
+        handle = handle_of(device) if fixed is None else fixed
+        if ws is not None and fixed is None and handle != home:
+            ws.record_stream(torch.cuda.current_stream(device))      # not handed out again before this call ends
+        st = fn(*args, handle)
         if st:
             _check(st, name)
     call.keep = keep         # the buffers outlive the callable
@@ -164,7 +179,7 @@ def _callable(name: str, args, keep):
 def bind_prepare(cfg: AttnConfig, cache: KVCache, qkv: torch.Tensor, q_norm_w: Optional[torch.Tensor],
                  k_norm_w: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
                  positions: Optional[torch.Tensor], slots: torch.Tensor, q_out: torch.Tensor, stream=None):
-    """moe_attn_prepare on these buffers, as a callable."""
+    """moe_attn_prepare on these buffers, as a callable (its stream: see the module)."""
     D, width = cfg.head_dim, (cfg.n_heads + 2 * cfg.n_kv_heads) * cfg.head_dim
     if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
         raise ValueError("qkv must be a [T, (n_heads + 2 n_kv_heads) * head_dim] tensor")
@@ -192,32 +207,34 @@ def bind_prepare(cfg: AttnConfig, cache: KVCache, qkv: torch.Tensor, q_norm_w: O
                 positions=positions, slots=slots, q_out=q_out)
     c, cc = cfg.c(), cache.c()
     args = (ctypes.byref(c), ctypes.byref(cc), qkv.data_ptr(), stride, T, _ptr(q_norm_w), _ptr(k_norm_w),
-            _ptr(cos_sin), P, _ptr(positions), slots.data_ptr(), q_out.data_ptr(), _stream(stream))
-    return _callable("moe_attn_prepare", args, (c, cc, cache, qkv, q_norm_w, k_norm_w, cos_sin, positions, slots,
-                                                q_out))
+            _ptr(cos_sin), P, _ptr(positions), slots.data_ptr(), q_out.data_ptr())
+    return _callable("moe_attn_prepare", args, stream, qkv.device.index,
+                     (c, cc, cache, qkv, q_norm_w, k_norm_w, cos_sin, positions, slots, q_out))
 
 
 def bind_decode(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor,
                 max_len: int, out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
-    """moe_attn_decode on these buffers, as a callable."""
+    """moe_attn_decode on these buffers, as a callable (its stream: see the module)."""
     B, n = (q.shape[0], q.shape[1]) if q.dim() == 4 else (-1, -1)
     _check_tensor(q, "q", (B, n, cfg.n_heads, cfg.head_dim), torch.bfloat16)
     _check_tensor(out, "out", tuple(q.shape), torch.bfloat16)
     pages = _check_sequences(cfg, cache, B, seq_lens, page_table)
-    if ws is None:
+    own = ws is None
+    if own:
         ws = _ws_on_stream(cfg, B * n, B, n, max_len, False, q.device, stream)
     _check_tensor(ws, "workspace", None, torch.uint8)
     _one_device(q=q, out=out, k=cache.k, v=cache.v, seq_lens=seq_lens, page_table=page_table, workspace=ws)
     c, cc = cfg.c(), cache.c()
     args = (ctypes.byref(c), ctypes.byref(cc), q.data_ptr(), B, n, seq_lens.data_ptr(), page_table.data_ptr(),
-            pages, int(max_len), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    return _callable("moe_attn_decode", args, (c, cc, cache, q, seq_lens, page_table, out, ws))
+            pages, int(max_len), out.data_ptr(), ws.data_ptr(), ws.numel())
+    return _callable("moe_attn_decode", args, stream, q.device.index, (c, cc, cache, q, seq_lens, page_table, out, ws),
+                     ws if own else None)
 
 
 def bind_prefill(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, max_q: int,
                  seq_lens: torch.Tensor, page_table: torch.Tensor, max_len: int, out: torch.Tensor,
                  ws: Optional[torch.Tensor] = None, stream=None):
-    """moe_attn_prefill on these buffers, as a callable."""
+    """moe_attn_prefill on these buffers, as a callable (its stream: see the module)."""
     T = q.shape[0] if q.dim() == 3 else -1
     _check_tensor(q, "q", (T, cfg.n_heads, cfg.head_dim), torch.bfloat16)
     _check_tensor(out, "out", tuple(q.shape), torch.bfloat16)
@@ -226,15 +243,17 @@ def bind_prefill(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, cu_q: torch.T
         raise ValueError("cu_q must be a [B + 1] tensor")
     _check_tensor(cu_q, "cu_q", (B + 1,), torch.int32)
     pages = _check_sequences(cfg, cache, B, seq_lens, page_table)
-    if ws is None:
+    own = ws is None
+    if own:
         ws = _ws_on_stream(cfg, T, B, max_q, max_len, True, q.device, stream)
     _check_tensor(ws, "workspace", None, torch.uint8)
     _one_device(q=q, out=out, k=cache.k, v=cache.v, cu_q=cu_q, seq_lens=seq_lens, page_table=page_table,
                 workspace=ws)
     c, cc = cfg.c(), cache.c()
     args = (ctypes.byref(c), ctypes.byref(cc), q.data_ptr(), T, cu_q.data_ptr(), B, int(max_q), seq_lens.data_ptr(),
-            page_table.data_ptr(), pages, int(max_len), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    return _callable("moe_attn_prefill", args, (c, cc, cache, q, cu_q, seq_lens, page_table, out, ws))
+            page_table.data_ptr(), pages, int(max_len), out.data_ptr(), ws.data_ptr(), ws.numel())
+    return _callable("moe_attn_prefill", args, stream, q.device.index,
+                     (c, cc, cache, q, cu_q, seq_lens, page_table, out, ws), ws if own else None)
 
 
 def _check_sequences(cfg, cache, B, seq_lens, page_table) -> int:

@@ -1,6 +1,7 @@
 """GPU tests of what a call of the attention operators promises beside its
 ordinary use: bounds below the lengths, values that are not finite, batches far
-more ragged than usual, one workspace for calls of many sizes."""
+more ragged than usual, one workspace for calls of many sizes, the stream that a
+bound call runs on."""
 import pytest
 import torch
 
@@ -115,3 +116,77 @@ def test_one_workspace_for_calls_of_many_sizes(heads, kv, dim):
                 A.moe_attn_decode(cfg, cache_of(b), q.view(shape), n, table, max(lens), out.view(shape), ws)
             assert torch.all(ws[need:] == 255), "the call wrote behind the bytes that it asks for"
             check(b, out, f"{form} with one workspace")
+
+
+def bound_calls(b):
+    """Bound decode and prefill (both in parts) of one batch of single tokens, and what they read and write."""
+    q = b.q.to(DEV)
+    lens, table = torch.tensor(b.lens, dtype=torch.int32, device=DEV), b.table.to(DEV)
+    cu = torch.arange(len(b.lens) + 1, dtype=torch.int32, device=DEV)
+    outs = [torch.zeros_like(q), torch.zeros_like(q)]
+    q4, o4 = q.view(-1, 1, *q.shape[1:]), outs[0].view(-1, 1, *q.shape[1:])
+    cache = cache_of(b)
+    return q, outs, [A.bind_decode(b.cfg, cache, q4, lens, table, max(b.lens), o4),
+                     A.bind_prefill(b.cfg, cache, q, cu, 1, lens, table, max(b.lens), outs[1])]
+
+
+def test_bound_calls_run_on_the_stream_of_the_call():
+    """Bound under one stream and called under another that is still busy making the queries."""
+    b = make_batch(config(8, 2, 128, 16), [5000, 333], [1, 1], seed=21)
+    print("[case] bound calls under another stream", flush=True)
+    q, outs, calls = bound_calls(b)
+    first = q.clone()
+    q.zero_()
+    x = torch.randn((8192, 8192), device=DEV).to(torch.bfloat16)
+    x @ x
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            x @ x                                    # about 20 ms
+        q.copy_(first)
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    for out, name in zip(outs, ("decode", "prefill")):
+        got, row = out.double().cpu().numpy(), 0
+        for i, (want, bound) in enumerate(b.expected()):
+            assert_within(got[row:row + 1], want, bound, f"bound {name} under another stream, sequence {i}")
+            row += 1
+
+
+def test_bound_calls_are_captured_under_the_capturing_stream():
+    """Bound before, under the default stream, and captured: every replay writes the outputs."""
+    b = make_batch(config(8, 2, 128, 16), [5000, 333], [1, 1], seed=23)
+    print("[case] bound calls in a graph", flush=True)
+    q, outs, calls = bound_calls(b)
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c in calls:
+            c()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o.view(torch.int16), w.view(torch.int16))
+
+
+def test_bound_calls_refuse_another_device(monkeypatch):
+    b = make_batch(config(8, 2, 128, 16), [50], [1], seed=24)
+    print("[case] bound calls, another device", flush=True)
+    other, now = 0, torch._C._cuda_getDevice
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now() + other)
+    calls = bound_calls(b)[2]
+    other = 1
+    for c in calls:
+        with pytest.raises(ValueError):
+            c()
+    other = 0
+    torch.cuda.synchronize()
