@@ -29,10 +29,19 @@ def hipcc():
 
 
 def build(verbose=False):
-    """Compile both sources side by side and link them into LIB."""
+    """Compile both sources side by side and link them into LIB; no object stays behind, of which one could be
+    linked into something else after its sources have changed."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    base = [hipcc()] + HIPCC_FLAGS
     objs = [os.path.join(LIB_DIR, os.path.basename(src)[:-4] + ".o") for src in (SRC, ATTN_SRC)]
+    try:
+        return _build([hipcc()] + HIPCC_FLAGS, objs, verbose)
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
+
+
+def _build(base, objs, verbose):
     jobs = []
     for src, obj in zip((SRC, ATTN_SRC), objs):
         cmd = [f for f in base if f != "-shared"] + ["-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
