@@ -135,7 +135,9 @@ int moe_attn_workspace_bound(const moe_attn_config* cfg, int64_t T, int64_t B, i
  *   seq_lens  [B] int32, the new tokens included, at most max_len.
  *   page_table [B, max_pages] int32.
  *   max_len   0 .. max_pages * page_size; longer sequences are cut to it.
- *             It sets the launch, not the work: a close bound is faster.
+ *             It sets the launch, not the work, and a close bound is faster: 2000
+ *             keys of 32/8 heads of 128 dims, bound 131072 or 2000: 20 and 9.9 us
+ *             of one sequence, 31 and 26 us of 16, 133 and 82 us of 64.
  */
 int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,
                     int64_t n_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,

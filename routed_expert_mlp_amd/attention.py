@@ -13,7 +13,8 @@ callable that issues the call again on the same buffers (serving loops).  It
 goes to the stream given when binding; with none given, to torch's current
 stream of the buffers' device at the time of each call, so that it can be
 called, or captured, under another stream than it was bound under.  Calls of one
-callable share its workspace: two of them must not run at the same time.
+callable share its workspace: two of them must not run at the same time, and a
+graph that has captured one needs the callable for as long as it is replayed.
 """
 from __future__ import annotations
 

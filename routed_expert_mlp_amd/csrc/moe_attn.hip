@@ -178,10 +178,10 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
   // the join 4 us and the partial sums' way out and back.  Parts of one size that
   // have places at once, or as many as there are places if all blocks were as
   // long as the longest may be; none shorter than PF_LEAST tiles.  32/8 heads: 512
-  // tokens behind 65024 cached ones 473 us, and 1255 us whole; 64 behind 7168
-  // 25 and 141 us, behind 1024 14.5 and 23 us; 8 pieces of 8/2 heads of 256 dims
-  // behind prefixes (178 blocks at most) 82 and 116 us; but 1024 tokens of a
-  // prompt 23.4 us whole, and 28.8 us in two parts.
+  // tokens behind 65024 cached ones 466 us, and 1248 us whole; 64 behind 7168
+  // 23 and 123 us, behind 1024 14.3 and 23 us; 8 pieces of 8/2 heads of 256 dims
+  // behind prefixes 71 and 108 us; but 1024 tokens of a prompt 23.3 us whole, and
+  // 28.8 us in two parts.
   constexpr int64_t TILE_NS = D == 64 ? 600 : D == 256 ? 780 : NW == 8 ? 1900 : 550;
   const int64_t places = 256 * S::PER_CU, rows = std::min(T, B * max_q) * c->n_heads;
   int64_t size = tiles, best = tiles * TILE_NS * (busy > 256 ? 8 : 5) / 5;
@@ -212,10 +212,10 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
 // 128 dims a block has 8 wavefronts, which share a tile's transfers, or 4 with
 // tiles of 32 keys, two blocks a CU, of which one starts or ends while the other
 // computes.  Long blocks that fill the GPU for 16 tiles want the former (32/8
-// heads: 4096 tokens 128 us, and 142 us with 4; 512 tokens behind 65024 470 and
-// 522 us, behind 3072 42.1 and 44.3 us), short or few ones the latter (2048 tokens
-// 48 us, and 53 us with 8; a window of 1024 on 8192 tokens 144 and 154 us; 256
-// tokens behind 3072 27.3 and 30.0 us; 16 behind 8176 23 and 26 us).  Other widths
+// heads: 4096 tokens 130 us, and 144 us with 4; 512 tokens behind 65024 466 and
+// 533 us, behind 3072 41.4 and 44.5 us), short or few ones the latter (2048 tokens
+// 48 us, and 51 us with 8; a window of 1024 on 8192 tokens 151 and 159 us; 256
+// tokens behind 3072 27.3 and 29.5 us; 16 behind 8176 16.3 and 19.5 us).  Other widths
 // have one form.
 template <typename F>
 int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
