@@ -10,6 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "moe_mlp.hip")
 ATTN_SRC = os.path.join(HERE, "csrc", "moe_attn.hip")
+PROJ_SRC = os.path.join(HERE, "csrc", "moe_proj.hip")
+SOURCES = (SRC, ATTN_SRC, PROJ_SRC)
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmoe_mlp.so")
 
@@ -29,10 +31,10 @@ def hipcc():
 
 
 def build(verbose=False):
-    """Compile both sources side by side and link them into LIB; no object stays behind, of which one could be
+    """Compile the sources side by side and link them into LIB; no object stays behind, of which one could be
     linked into something else after its sources have changed."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    objs = [os.path.join(LIB_DIR, os.path.basename(src)[:-4] + ".o") for src in (SRC, ATTN_SRC)]
+    objs = [os.path.join(LIB_DIR, os.path.basename(src)[:-4] + ".o") for src in SOURCES]
     try:
         return _build([hipcc()] + HIPCC_FLAGS, objs, verbose)
     finally:
@@ -43,7 +45,7 @@ def build(verbose=False):
 
 def _build(base, objs, verbose):
     jobs = []
-    for src, obj in zip((SRC, ATTN_SRC), objs):
+    for src, obj in zip(SOURCES, objs):
         cmd = [f for f in base if f != "-shared"] + ["-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)

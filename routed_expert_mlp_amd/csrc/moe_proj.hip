@@ -1,0 +1,206 @@
+// C ABI of the operators around the halves of the layer (declarations and
+// contract in include/moe_proj.h).  Host code: argument validation before
+// anything is enqueued, and the launches.  Nothing here allocates, synchronises
+// or keeps state.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_proj.h"
+#include "proj_fp8.hpp"
+#include "proj_lora.hpp"
+#include "proj_norm.hpp"
+
+namespace {
+
+using namespace moe;
+
+constexpr int64_t kInt32End = int64_t(1) << 31;
+constexpr int64_t kMaxTokens = int64_t(1) << 23;   // rows of one call: a block of 512 threads each stays a grid
+
+bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// hipLaunchKernel says whether this launch failed; an error that an earlier
+// call of the process left behind is not taken for it.
+template <typename A>
+int launch(void (*kernel)(A), dim3 grid, dim3 block, hipStream_t s, A args) {
+  void* p[] = {&args};
+  if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, p, 0, s) == hipSuccess)
+    return MOE_MLP_OK;
+  (void)hipGetLastError();
+  return MOE_MLP_ERR_HIP;
+}
+
+bool features_ok(int64_t n, int64_t multiple) { return n >= multiple && n < MOE_PROJ_MAX_FEATURES && n % multiple == 0; }
+
+bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride < kInt32End && stride % 8 == 0; }
+
+template <int WPR>
+int norm(const NormArgs& a, hipStream_t s) {
+  const int pieces = static_cast<int>(cdiv(a.hidden, 8 * 64 * WPR));
+  const dim3 grid(static_cast<unsigned>(WPR == 1 ? cdiv(a.T, 4) : a.T)), block(WPR == 1 ? 256 : WPR * 64);
+  if (pieces <= 1) return launch(k_proj_norm<WPR, 1>, grid, block, s, a);
+  if (pieces <= 2) return launch(k_proj_norm<WPR, 2>, grid, block, s, a);
+  return launch(k_proj_norm<WPR, 4>, grid, block, s, a);
+}
+
+// How the adapters' products are cut.
+struct LoraPlan {
+  int64_t windows, parts, part_chunks;
+  int slots_down, slots_up, groups, col_blocks;
+  size_t ws_bytes;
+};
+
+// Parts of the sum over the input that fill the GPU with windows of 64 tokens; none shorter than a chunk for each
+// wavefront of a block.
+int64_t lora_parts(int64_t windows, int64_t chunks) {
+  return std::max<int64_t>(1, std::min(cdiv(chunks, 4), 512 / windows));
+}
+
+LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
+  LoraPlan p{};
+  const int64_t chunks = cdiv(d->in_features, 64);
+  p.windows = cdiv(T, LORA_WINDOW);
+  p.part_chunks = cdiv(chunks, lora_parts(p.windows, chunks));
+  p.parts = cdiv(chunks, p.part_chunks);
+  p.groups = static_cast<int>(cdiv(d->max_rank, 16 * LORA_RT));
+  p.col_blocks = static_cast<int>(cdiv(d->out_features, 256));
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(LORA_WINDOW, T), d->n_adapters);
+  p.slots_down = static_cast<int>(std::max<int64_t>(1, std::min(most, 1024 / p.windows)));
+  p.slots_up = static_cast<int>(std::max<int64_t>(1, std::min(most, 2048 / (p.windows * p.col_blocks))));
+  // of T tokens or fewer: parts are at most ceil(chunks / 4), and more than one only while parts x windows <= 512
+  const int64_t rows = std::min(T * cdiv(chunks, 4), std::max<int64_t>(T, 512 * LORA_WINDOW));
+  p.ws_bytes = size_t(rows) * (cdiv(d->max_rank, 16) * 16) * 4;
+  return p;
+}
+
+int validate_adapters(const moe_proj_adapters* d, int64_t T) {
+  if (!d) return MOE_MLP_ERR_NULL_ARG;
+  if (T < 0 || T >= kMaxTokens) return MOE_MLP_ERR_BAD_SHAPE;
+  if (d->n_adapters < 1 || d->n_adapters > (int64_t(1) << 20)) return MOE_MLP_ERR_BAD_SHAPE;
+  if (d->max_rank < 8 || d->max_rank > MOE_PROJ_LORA_MAX_RANK || d->max_rank % 8 != 0) return MOE_MLP_ERR_BAD_SHAPE;
+  if (!features_ok(d->in_features, 8) || !features_ok(d->out_features, 8)) return MOE_MLP_ERR_BAD_SHAPE;
+  return MOE_MLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_proj_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, const float* weight, float eps,
+                  int64_t T, int64_t hidden, uint16_t* h_out, uint16_t* y_out, uint8_t* q_out, float* q_scale,
+                  void* stream) {
+  if (T < 0 || T >= kMaxTokens || hidden < 8 || hidden % 8 != 0 || hidden > MOE_PROJ_NORM_MAX_HIDDEN ||
+      !stride_ok(x_stride, hidden))
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.0f) return MOE_MLP_ERR_BAD_VALUE;
+  if ((!y_out && !q_out) || !q_out != !q_scale) return MOE_MLP_ERR_NULL_ARG;
+  if (T == 0) return MOE_MLP_OK;
+  if (!x) return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(x) || !aligned(residual) || !aligned(weight) || !aligned(h_out) || !aligned(y_out) || !aligned(q_out) ||
+      !aligned(q_scale))
+    return MOE_MLP_ERR_MISALIGNED;
+  // an output row written into x has to be that row
+  if ((h_out == x || y_out == x) && x_stride != hidden) return MOE_MLP_ERR_BAD_VALUE;
+  if (h_out && h_out == y_out) return MOE_MLP_ERR_BAD_VALUE;
+  NormArgs a{};
+  a.x = x;
+  a.r = residual;
+  a.w = weight;
+  a.h = h_out;
+  a.y = y_out;
+  a.q = q_out;
+  a.s = q_scale;
+  a.x_stride = x_stride;
+  a.T = T;
+  a.hidden = static_cast<int32_t>(hidden);
+  a.blocks = static_cast<int32_t>(cdiv(hidden, 128));
+  a.eps = eps;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (hidden <= 1024) return norm<1>(a, s);
+  if (hidden <= 8192) return norm<4>(a, s);
+  return norm<8>(a, s);
+}
+
+int moe_proj_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale, int64_t T, int64_t N,
+                 int64_t K, uint16_t* y, void* stream) {
+  if (T < 0 || T >= kMaxTokens || !features_ok(N, 16) || !features_ok(K, 128) || T * N >= int64_t(1) << 32)
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (T == 0) return MOE_MLP_OK;
+  if (!x || !x_scale || !w || !w_scale || !y) return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(x) || !aligned(x_scale) || !aligned(w) || !aligned(w_scale) || !aligned(y)) return MOE_MLP_ERR_MISALIGNED;
+  Fp8Args a{};
+  a.x = x;
+  a.xs = x_scale;
+  a.w = w;
+  a.ws = w_scale;
+  a.y = y;
+  a.T = T;
+  a.N = static_cast<int32_t>(N);
+  a.K = static_cast<int32_t>(K);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned blocks = static_cast<unsigned>(N / 16 * cdiv(T, 64));
+  if (T <= 16) return launch(k_proj_fp8_few<1, 8>, dim3(blocks), dim3(512), s, a);
+  if (T <= 32) return launch(k_proj_fp8_few<2, 8>, dim3(blocks), dim3(512), s, a);
+  return launch(k_proj_fp8_few<4, 8>, dim3(blocks), dim3(512), s, a);
+}
+
+int moe_proj_lora_workspace_size(const moe_proj_adapters* adapters, int64_t T, size_t* bytes) {
+  const int st = validate_adapters(adapters, T);
+  if (st) return st;
+  if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = T ? lora_plan(adapters, T).ws_bytes : 0;
+  return MOE_MLP_OK;
+}
+
+int moe_proj_lora(const moe_proj_adapters* adapters, const uint16_t* x, int64_t x_stride, int64_t T,
+                  const int32_t* adapter, const uint16_t* base, int64_t base_stride, uint16_t* out,
+                  int64_t out_stride, void* workspace, size_t ws_bytes, void* stream) {
+  const moe_proj_adapters* d = adapters;
+  const int st = validate_adapters(d, T);
+  if (st) return st;
+  if (!stride_ok(x_stride, d->in_features) || !stride_ok(base_stride, d->out_features) ||
+      !stride_ok(out_stride, d->out_features))
+    return MOE_MLP_ERR_BAD_SHAPE;
+  if (T == 0) return MOE_MLP_OK;
+  if (!d->a || !d->b || !x || !adapter || !base || !out || !workspace) return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(d->a) || !aligned(d->b) || !aligned(d->ranks, 4) || !aligned(d->scales, 4) || !aligned(x) ||
+      !aligned(adapter, 4) || !aligned(base) || !aligned(out) || !aligned(workspace))
+    return MOE_MLP_ERR_MISALIGNED;
+  if (out == base && out_stride != base_stride) return MOE_MLP_ERR_BAD_VALUE;
+  const LoraPlan p = lora_plan(d, T);
+  if (ws_bytes < p.ws_bytes) return MOE_MLP_ERR_WORKSPACE_TOO_SMALL;
+  LoraArgs a{};
+  a.a = d->a;
+  a.b = d->b;
+  a.ranks = d->ranks;
+  a.scales = d->scales;
+  a.x = x;
+  a.adapter = adapter;
+  a.base = base;
+  a.out = out;
+  a.v = static_cast<float*>(workspace);
+  a.x_stride = x_stride;
+  a.base_stride = base_stride;
+  a.out_stride = out_stride;
+  a.T = T;
+  a.n_adapters = d->n_adapters;
+  a.R = d->max_rank;
+  a.K = d->in_features;
+  a.N = d->out_features;
+  a.vr = static_cast<int32_t>(cdiv(d->max_rank, 16) * 16);
+  a.parts = static_cast<int32_t>(p.parts);
+  a.part_chunks = static_cast<int32_t>(p.part_chunks);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  a.slots = p.slots_down;
+  const int sd = launch(k_lora_down, dim3(static_cast<unsigned>(p.windows * p.slots_down), static_cast<unsigned>(p.parts),
+                                          static_cast<unsigned>(p.groups)), dim3(256), s, a);
+  if (sd) return sd;
+  a.slots = p.slots_up;
+  return launch(k_lora_up, dim3(static_cast<unsigned>(p.windows * p.slots_up), static_cast<unsigned>(p.col_blocks)),
+                dim3(256), s, a);
+}
+
+}  // extern "C"

@@ -1,0 +1,134 @@
+// The residual's addition, the RMS norm of the row and its E4M3 form, in one pass.
+//
+//   h = x + r;  y = h rsqrt(mean(h^2) + eps) w;  per 128 columns s = max|y| / 448, q = e4m3(y / s)
+//
+// What bounds it: every value is read and written once, for a dozen operations;
+// with few rows, the launch.  So a row is read into registers, WPR wavefronts of
+// NV pieces of 8 values a lane, its squares are summed (over the wavefronts in
+// LDS), and everything that is asked for goes out from there.  16 neighbouring
+// lanes hold the 128 columns of a scale.
+//
+// The sum, the norm and the scales are in fp32; h and y are each rounded once to
+// bf16, the type of the layer's rows, and q once to E4M3, from y before its
+// rounding.
+#pragma once
+
+#include "common.hpp"
+
+namespace moe {
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* r;
+  const float* w;
+  uint16_t* h;
+  uint16_t* y;
+  uint8_t* q;
+  float* s;
+  int64_t x_stride, T;
+  int32_t hidden, blocks;    // columns; scales of a row
+  float eps;
+};
+
+__device__ __forceinline__ float dpp_max(float v, int o) { return fmaxf(v, __int_as_float(o)); }
+
+// Largest of the 16 lanes of a row.
+__device__ __forceinline__ float row_max(float v) {
+  v = dpp_max(v, dpp_mov<DPP_QUAD_1032>(__float_as_int(v)));
+  v = dpp_max(v, dpp_mov<DPP_QUAD_2301>(__float_as_int(v)));
+  v = dpp_max(v, dpp_mov<DPP_ROW_HALF_MIRROR>(__float_as_int(v)));
+  return dpp_max(v, dpp_mov<DPP_ROW_MIRROR>(__float_as_int(v)));
+}
+
+// Four values to E4M3 bytes, nearest even; |v| < 464, or NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+}
+
+__device__ __forceinline__ void bf16x8_to_f32(uint4 v, float (&f)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&f)[8]) {
+  return uint4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
+// WPR wavefronts a row (1: four rows a block), NV pieces of 8 values a lane.
+template <int WPR, int NV>
+__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_proj_norm(NormArgs a) {
+  constexpr int RPB = WPR == 1 ? 4 : 1, LANES = WPR * 64;
+  const int lane = threadIdx.x % LANES;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LANES;
+  if (RPB > 1 && t >= a.T) return;
+  const int pieces = a.hidden / 8;
+  const uint4* const x = reinterpret_cast<const uint4*>(a.x + t * a.x_stride);
+  const int64_t row = t * pieces;
+  float v[NV][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = lane + LANES * i;
+    const bool in = p < pieces;
+    uint4 raw = {}, res = {};
+    if (in) raw = x[p];
+    if (in && a.r) res = reinterpret_cast<const uint4*>(a.r)[row + p];
+    bf16x8_to_f32(raw, v[i]);
+    if (a.r) {
+      float f[8];
+      bf16x8_to_f32(res, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] += f[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+  }
+  sum = wave_sum(sum);
+  if constexpr (WPR > 1) {
+    __shared__ float part[WPR];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = part[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) sum += part[i];
+  }
+  const float inv = 1.0f / sqrtf(sum / static_cast<float>(a.hidden) + a.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = lane + LANES * i;
+    const bool in = p < pieces;
+    if (in && a.h) reinterpret_cast<uint4*>(a.h)[row + p] = f32_to_bf16x8(v[i]);
+    if (in && a.w) {
+      const f32x4 w0 = reinterpret_cast<const f32x4*>(a.w)[2 * p], w1 = reinterpret_cast<const f32x4*>(a.w)[2 * p + 1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[i][j] *= inv * w0[j];
+        v[i][4 + j] *= inv * w1[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+    }
+    if (in && a.y) reinterpret_cast<uint4*>(a.y)[row + p] = f32_to_bf16x8(v[i]);
+    if (a.q) {
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+      top = row_max(top);              // lanes past the row's end have zeros
+      const float s = fmaxf(top / 448.0f, 1.17549435e-38f), to = 1.0f / s;
+      if (in) {
+        reinterpret_cast<uint2*>(a.q)[row + p] =
+            uint2{pack_e4m3x4(v[i][0] * to, v[i][1] * to, v[i][2] * to, v[i][3] * to),
+                  pack_e4m3x4(v[i][4] * to, v[i][5] * to, v[i][6] * to, v[i][7] * to)};
+        if ((lane & 15) == 0) a.s[t * a.blocks + p / 16] = s;
+      }
+    }
+  }
+}
+
+}  // namespace moe
