@@ -144,7 +144,35 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
                     int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
- * The same for prompts, or pieces of prompts behind a cached prefix: sequence
+ * moe_attn_decode for a batch whose sequences begin with the same shared_len
+ * tokens, which are cached once: their keys and values are read once for the new
+ * tokens of all sequences, not once for each.  The same results as
+ * moe_attn_decode with those pages in every row of the table, but for the order
+ * of the sums.
+ *   shared_pages [ceil(shared_len / page_size)] int32: the pages of the tokens
+ *             0 .. shared_len - 1 (NULL only when shared_len is 0).
+ *   shared_len 0 .. max_len, any number: token shared_len of sequence b is its own
+ *             and sits in page page_table[b][shared_len / page_size], so that a
+ *             prefix that ends inside a page is in one shared page and the
+ *             sequences' tokens behind it in pages of theirs.  Entries of the page
+ *             table before that one are not used (they may name the shared pages,
+ *             as the table of moe_attn_decode does, or nothing).
+ *   seq_lens  [B] int32, the prefix and the new tokens included.  A sequence that
+ *             ends inside the prefix (0: a padded row) sees what it has of it.
+ * Everything else as moe_attn_decode; one prefix a call.  Worth it where the prefix
+ * is long against B times a block's start.
+ */
+int moe_attn_decode_shared(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,
+                           int64_t n_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
+                           int64_t max_len, const int32_t* shared_pages, int64_t shared_len, uint16_t* out,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_attn_decode_shared for these sizes.  `bytes` is a HOST pointer.  Limits as for decode. */
+int moe_attn_shared_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t n_q, int64_t max_len,
+                                   int64_t shared_len, size_t* bytes);
+
+/*
+ * moe_attn_decode for prompts, or pieces of prompts behind a cached prefix: sequence
  * b has the new tokens cu_q[b] .. cu_q[b+1]-1 of q, the last ones of its
  * seq_lens[b] tokens, all of them in the cache already.
  *   q         [T, n_heads, head_dim] bf16;  out the same shape (rows outside

@@ -2,13 +2,14 @@
 
 The attention half of the decoder layer whose MLP half capi.py binds: head
 norms, rotation and cache append of new tokens (moe_attn_prepare), attention of
-a few new tokens per sequence over the paged cache (moe_attn_decode) and of
-prompts or pieces of prompts (moe_attn_prefill).  As in capi.py, every function
+a few new tokens per sequence over the paged cache (moe_attn_decode), of a batch
+that shares a prefix (moe_attn_decode_shared), and of prompts or pieces of prompts
+(moe_attn_prefill).  As in capi.py, every function
 checks dtype, shape, device and contiguity of its tensors, passes their device
 pointers and torch's current HIP stream, and raises MoeMlpError on a non-zero
 status; the library does all of the computing.
 
-bind_prepare, bind_decode and bind_prefill check and marshal once and return a
+bind_prepare, bind_decode, bind_decode_shared and bind_prefill check and marshal once and return a
 callable that issues the call again on the same buffers (serving loops).  It
 goes to the stream given when binding; with none given, to torch's current
 stream of the buffers' device at the time of each call, so that it can be
@@ -33,7 +34,7 @@ MAX_HEADS = 1024
 DECODE_MAX_Q = 8
 
 EXPORTED = ("moe_attn_prepare", "moe_attn_workspace_size", "moe_attn_workspace_bound", "moe_attn_decode",
-            "moe_attn_prefill")
+            "moe_attn_prefill", "moe_attn_decode_shared", "moe_attn_shared_workspace_size")
 
 
 class moe_attn_config(ctypes.Structure):
@@ -60,6 +61,8 @@ def _lib() -> ctypes.CDLL:
         L.moe_attn_workspace_size.argtypes = [cfgp, i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(sz)]
         L.moe_attn_workspace_bound.argtypes = L.moe_attn_workspace_size.argtypes
         L.moe_attn_decode.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
+        L.moe_attn_decode_shared.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, i64, vp, vp, sz, vp]
+        L.moe_attn_shared_workspace_size.argtypes = [cfgp, i64, i64, i64, i64, ctypes.POINTER(sz)]
         L.moe_attn_prefill.argtypes = [cfgp, cp, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         for n in EXPORTED:
             getattr(L, n).restype = ctypes.c_int
@@ -139,6 +142,15 @@ def workspace(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill
                        device=device)
 
 
+def moe_attn_shared_workspace_size(cfg: AttnConfig, B: int, n_q: int, max_len: int, shared_len: int) -> int:
+    """Bytes of moe_attn_decode_shared for n_q new tokens of B sequences of at most max_len tokens, the first shared_len
+    of which they share."""
+    n = ctypes.c_size_t(0)
+    _check(_lib().moe_attn_shared_workspace_size(ctypes.byref(cfg.c()), int(B), int(n_q), int(max_len), int(shared_len),
+                                                 ctypes.byref(n)), "moe_attn_shared_workspace_size")
+    return n.value
+
+
 def _one_device(**tensors) -> None:
     here = torch.cuda.current_device()
     for name, t in tensors.items():
@@ -147,12 +159,16 @@ def _one_device(**tensors) -> None:
 
 
 def _ws_on_stream(cfg, T, B, max_q, max_len, prefill, device, stream) -> torch.Tensor:
+    return _bytes_on_stream(moe_attn_workspace_size(cfg, T, B, max_q, max_len, prefill), device, stream)
+
+
+def _bytes_on_stream(n: int, device, stream) -> torch.Tensor:
     """A workspace that torch's allocator ties to the stream that the call runs on."""
     handle = _stream(stream)
     if handle == torch.cuda.current_stream().cuda_stream:
-        return workspace(cfg, T, B, max_q, max_len, prefill, device)
+        return torch.empty(max(1, n), dtype=torch.uint8, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
-        return workspace(cfg, T, B, max_q, max_len, prefill, device)
+        return torch.empty(max(1, n), dtype=torch.uint8, device=device)
 
 
 def _callable(name: str, args, stream, device: int, keep, ws: Optional[torch.Tensor] = None):
@@ -232,6 +248,32 @@ def bind_decode(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: torc
                      ws if own else None)
 
 
+def bind_decode_shared(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor,
+                       page_table: torch.Tensor, max_len: int, shared_pages: Optional[torch.Tensor], shared_len: int,
+                       out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
+    """moe_attn_decode_shared on these buffers, as a callable (its stream: see the module)."""
+    B, n = (q.shape[0], q.shape[1]) if q.dim() == 4 else (-1, -1)
+    _check_tensor(q, "q", (B, n, cfg.n_heads, cfg.head_dim), torch.bfloat16)
+    _check_tensor(out, "out", tuple(q.shape), torch.bfloat16)
+    pages = _check_sequences(cfg, cache, B, seq_lens, page_table)
+    if shared_pages is not None:
+        need = -(-int(shared_len) // cfg.page_size)
+        if shared_pages.dim() != 1 or shared_pages.shape[0] < need:
+            raise ValueError(f"shared_pages: shape {tuple(shared_pages.shape)}, expected at least {need} pages")
+        _check_tensor(shared_pages, "shared_pages", None, torch.int32)
+    own = ws is None
+    if own:
+        ws = _bytes_on_stream(moe_attn_shared_workspace_size(cfg, B, n, max_len, shared_len), q.device, stream)
+    _check_tensor(ws, "workspace", None, torch.uint8)
+    _one_device(q=q, out=out, k=cache.k, v=cache.v, seq_lens=seq_lens, page_table=page_table,
+                shared_pages=shared_pages, workspace=ws)
+    c, cc = cfg.c(), cache.c()
+    args = (ctypes.byref(c), ctypes.byref(cc), q.data_ptr(), B, n, seq_lens.data_ptr(), page_table.data_ptr(),
+            pages, int(max_len), _ptr(shared_pages), int(shared_len), out.data_ptr(), ws.data_ptr(), ws.numel())
+    return _callable("moe_attn_decode_shared", args, stream, q.device.index,
+                     (c, cc, cache, q, seq_lens, page_table, shared_pages, out, ws), ws if own else None)
+
+
 def bind_prefill(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, max_q: int,
                  seq_lens: torch.Tensor, page_table: torch.Tensor, max_len: int, out: torch.Tensor,
                  ws: Optional[torch.Tensor] = None, stream=None):
@@ -277,6 +319,13 @@ def moe_attn_decode(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: 
                     stream=None) -> None:
     """Attention of the last q.shape[1] tokens of every sequence over the cache: q, out [B, n_q, n_heads, head_dim]."""
     bind_decode(cfg, cache, q, seq_lens, page_table, max_len, out, ws, stream)()
+
+
+def moe_attn_decode_shared(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor,
+                           page_table: torch.Tensor, max_len: int, shared_pages: Optional[torch.Tensor],
+                           shared_len: int, out: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_attn_decode of sequences that begin with the same shared_len tokens, which sit in shared_pages once."""
+    bind_decode_shared(cfg, cache, q, seq_lens, page_table, max_len, shared_pages, shared_len, out, ws, stream)()
 
 
 def moe_attn_prefill(cfg: AttnConfig, cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, max_q: int,

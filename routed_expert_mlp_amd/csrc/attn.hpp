@@ -32,6 +32,15 @@ struct AttnArgs {
   int32_t col_blocks;         // prefill: column blocks of all sequences (at most)
   int32_t ws_cols;            // prefill: columns that a block has in the workspace
   float scale_log2;           // scale * log2(e): the softmax runs on exp2
+  // decode behind a shared prefix (attn_shared.hpp); splits, tiles_per_split and ws are then those of the
+  // sequences' own keys
+  const int32_t* shared_pages;
+  float* ml;                  // maxima and sums of the parts of the own keys
+  float* pws;                 // parts of the prefix: sums,
+  float* pml;                 // maxima and sums
+  int32_t shared;             // keys of the prefix
+  int32_t p_splits, p_tiles_per_split;
+  int32_t p_blocks;           // blocks of k_attn_decode that take the prefix: its first ones
 };
 
 // New tokens of a sequence that are computed (rows row0 .. row0 + n - 1 of q),
@@ -81,8 +90,9 @@ struct AttnTiles {
   }
   // Keeps part `split` of parts of `size` tiles; false if there is none, except for an empty first one.
   __device__ __forceinline__ bool keep_part(int split, int size) {
-    skip = split * size;
-    n = min(n - skip, size);
+    const int before = split * size;
+    skip += before;
+    n = min(n - before, size);
     if (n > 0) return true;
     n = 0;
     return split == 0;
@@ -103,6 +113,55 @@ __device__ __forceinline__ AttnTiles attn_tiles(const AttnArgs& a, int first, in
   t.b0 = uniform(t.b0);
   t.skip = 0;
   return t;
+}
+
+// The same of the keys key0 .. hi - 1 alone, of which some positions see those from lo on and the sinks; `skip` then
+// counts the tiles before key0 too.
+template <int TS>
+__device__ __forceinline__ AttnTiles attn_tiles_between(const AttnArgs& a, int key0, int lo, int hi) {
+  AttnTiles t;
+  t.hi = uniform(hi);
+  t.lo = uniform(lo);
+  t.sinks = a.window ? a.sinks : 0;
+  const int start = key0 / TS, end = t.hi > key0 ? (t.hi + TS - 1) / TS : start;
+  int na = min(max((min(t.sinks, t.hi) + TS - 1) / TS, start), end), b0 = min(max(t.lo / TS, start), end);
+  if (na >= b0) na = b0 = start;
+  t.n = uniform(na - start + end - b0);
+  t.na = uniform(na);
+  t.b0 = uniform(b0);
+  t.skip = uniform(start);
+  return t;
+}
+
+// Positions of the new tokens of a batch that columns c0 .. c1 - 1 of a key/value head have: of this lane's column, and
+// the first and the last of all of them.
+struct AttnSpan {
+  int pos, first, last;
+};
+
+__device__ __forceinline__ int attn_position(const AttnArgs& a, int token) {
+  const int b = token / a.n_q;
+  return min(max(a.seq_lens[b], 0), a.max_len) - a.n_q + (token - b * a.n_q);
+}
+
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int col, int c0, int c1) {
+  AttnSpan s;
+  s.pos = attn_position(a, col / a.group);
+  const int t0 = c0 / a.group, t1 = (c1 - 1) / a.group;
+  int lo = 0x7FFFFFFF, hi = -0x7FFFFFFF;
+  for (int t = t0 + static_cast<int>(threadIdx.x & 63); t <= t1; t += 64) {
+    const int p = attn_position(a, t);
+    lo = min(lo, p);
+    hi = max(hi, p);
+  }
+#pragma unroll
+  for (int x = 32; x; x >>= 1) {
+    lo = min(lo, __shfl_xor(lo, x));
+    hi = max(hi, __shfl_xor(hi, x));
+  }
+  s.first = uniform(lo);
+  s.last = uniform(hi);
+  return s;
 }
 
 // 32x32x16 MFMA, C = A B: lane l holds column l % 32 and rows

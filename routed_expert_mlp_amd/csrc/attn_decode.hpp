@@ -59,10 +59,17 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int
 // half as many blocks, and wavefronts, a CU: 8 sequences of 8 new tokens of 64/2
 // heads 44 us, and 35 us in blocks of 32; 64 of 4 tokens of 64/4 heads 100 and
 // 107 us, the only case of many where they were faster.
-template <int D, bool AGAIN>
+//
+// BEHIND: behind a shared prefix.  The first p_blocks blocks take the prefix, with
+// the columns of the whole batch, the others each sequence's own keys; both leave
+// their parts to k_attn_shared_join.
+template <int D, bool AGAIN, bool BEHIND = false>
 __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_decode(AttnArgs a) {
   constexpr int NW = ATTN_NW, KS = D / 16, DT = D / 32, COLS = 32, LD = D + 4;
-  const int cols = a.n_q * a.group;
+  const bool lead = BEHIND && static_cast<int>(blockIdx.x) < a.p_blocks;
+  const int block = BEHIND && !lead ? static_cast<int>(blockIdx.x) - a.p_blocks : static_cast<int>(blockIdx.x);
+  const int sequences = lead ? 1 : a.B, tokens = lead ? a.B * a.n_q : a.n_q;
+  const int cols = tokens * a.group;
   const int col_blocks = (cols + COLS - 1) / COLS;
   // the parts of a sequence run slowest: with parts next to each other, the
   // later ones, which shorter sequences lack, would all fall to the same XCDs
@@ -71,12 +78,13 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
   // about the same time, so that its L2 has the keys for the second (64 sequences
   // of 4 new tokens, 64/4 heads of 256 dims, up to 4096 keys: 305 us next to each
   // other and around the caches, 237 us this way, 211 us through the caches too)
-  const int cb = static_cast<int>(blockIdx.x / 8) % col_blocks;
-  int bi = static_cast<int>(blockIdx.x / (8 * col_blocks)) * 8 + blockIdx.x % 8;
+  const int cb = static_cast<int>(static_cast<unsigned>(block) / 8) % col_blocks;
+  int bi = static_cast<int>(static_cast<unsigned>(block) / (8 * col_blocks)) * 8 + static_cast<unsigned>(block) % 8;
   const int kvh = bi % a.kv_heads;
   bi /= a.kv_heads;
-  const int b = bi % a.B, split = bi / a.B;
-  if (split >= a.splits) return;
+  const int b = bi % sequences, split = bi / sequences;
+  const int splits = lead ? a.p_splits : a.splits;
+  if (split >= splits) return;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
   const int w = uniform(tid >> 6);
   // the queries are on their way before the sequence's length is known
@@ -86,11 +94,37 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
   const uint16_t* qp = a.q + attn_row(a, static_cast<int64_t>(b) * a.n_q, kvh, col) * D + 8 * half;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
-  const AttnSeq s = attn_seq(a, b);
-  const int first = s.first;
-  AttnTiles tl = attn_tiles<32>(a, first, s.len - 1);
-  const bool whole = tl.n <= a.tiles_per_split;
-  if (!tl.keep_part(split, a.tiles_per_split)) return;
+  AttnSeq s;
+  AttnTiles tl;
+  int pos, first, see_last;      // of this lane's column; the first of all, which sees keys up to it; last key of a window's gap
+  bool whole = false;
+  const int32_t* pages = a.page_table + b * a.max_pages;
+  if constexpr (BEHIND) {
+    if (lead) {
+      const AttnSpan span = attn_span(a, col, cb * COLS, min(cb * COLS + COLS, cols));
+      s = AttnSeq{0, tokens, a.shared, 0};
+      pos = span.pos;
+      first = min(span.first, a.shared - 1);
+      see_last = attn_window_lo(a, span.last);
+      tl = attn_tiles_between<32>(a, 0, attn_window_lo(a, span.first), min(a.shared, span.last + 1));
+      pages = a.shared_pages;
+      if (!tl.keep_part(split, a.p_tiles_per_split)) tl.n = 0;
+    } else {
+      s = attn_seq(a, b);
+      first = s.first;
+      pos = first + tok;
+      see_last = max(0, s.len - a.window);
+      tl = attn_tiles_between<32>(a, a.shared, attn_window_lo(a, first), s.len);
+      if (!tl.keep_part(split, a.tiles_per_split)) return;
+    }
+  } else {
+    s = attn_seq(a, b);
+    first = s.first;
+    see_last = max(0, s.len - a.window);
+    tl = attn_tiles<32>(a, first, s.len - 1);
+    whole = tl.n <= a.tiles_per_split;
+    if (!tl.keep_part(split, a.tiles_per_split)) return;
+  }
 
   __shared__ int ids[2 * ATTN_MAX_TPS];
   __shared__ float lm[NW][COLS], ll[NW][COLS];
@@ -99,10 +133,10 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
   // page of each 16 keys of this part
   for (int i = tid; i < 2 * tl.n; i += NW * 64) {
     const int key = min(32 * tl.tile(i >> 1) + 16 * (i & 1), s.len - 1);
-    ids[i] = min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
+    ids[i] = min(max(pages[key >> a.page_shift], 0), a.n_pages - 1);
   }
 
-  const int pos = first + tok;
+  if constexpr (!BEHIND) pos = first + tok;
   __syncthreads();
 
   const int ps = 1 << a.page_shift;
@@ -154,15 +188,19 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
     const int key0 = 32 * tl.tile(v);
     // a tile that some column sees only in part: scores of invisible keys go to
     // -inf, and the values of keys that nobody sees, whatever the slots hold, to 0
-    if (key0 + 31 > first || (a.window && key0 < max(0, s.len - a.window) && key0 + 31 >= tl.sinks)) {
+    if (key0 + 31 > first || (a.window && key0 < see_last && key0 + 31 >= tl.sinks) ||
+        (BEHIND && !lead && key0 < a.shared)) {
+      // keys of the prefix are in neither the last tile of it nor the first own one twice
+      auto mine = [&](int k0) { return !BEHIND || lead ? ~uint64_t(0) : ~low_bits(a.shared - k0); };
       const uint32_t see = static_cast<uint32_t>(
-          visible_bits(key0 + 8 * half, pos, attn_window_lo(a, pos), tl.sinks));
+          visible_bits(key0 + 8 * half, lead ? min(pos, a.shared - 1) : pos, attn_window_lo(a, pos), tl.sinks) &
+          mine(key0 + 8 * half));
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[e] = keep_if(see, 16 * (e >> 3) + (e & 7), sc[e]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const uint4 mk = value_mask(static_cast<uint32_t>(
-            visible_bits(key0 + 16 * g + 8 * half, tl.hi - 1, tl.lo, tl.sinks)));
+            visible_bits(key0 + 16 * g + 8 * half, tl.hi - 1, tl.lo, tl.sinks) & mine(key0 + 16 * g + 8 * half)));
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) vf[g][dt] = and4(vf[g][dt], mk);
       }
@@ -252,10 +290,14 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
         *reinterpret_cast<uint2*>(o + 32 * dt + 8 * i) = p;
       }
   } else {
-    const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * a.splits + split;
-    const int64_t items = static_cast<int64_t>(a.B) * a.kv_heads * cols * a.splits;
-    if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + item * 2) = float2{M, L};
-    float* o = a.ws + item * D + 4 * half;
+    const int64_t item = ((static_cast<int64_t>(b) * a.kv_heads + kvh) * cols + col) * splits + split;
+    float* const sums = lead ? a.pws : a.ws;
+    float* ml;
+    if constexpr (BEHIND) ml = lead ? a.pml : a.ml;
+    else ml = a.ws + static_cast<int64_t>(a.B) * a.kv_heads * cols * splits * D;
+    if (half == 0) *reinterpret_cast<float2*>(ml + item * 2) = float2{M, L};
+    if (BEHIND && tl.n == 0) return;             // a part without keys has a sum of 0, and its values are not read
+    float* o = sums + item * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll

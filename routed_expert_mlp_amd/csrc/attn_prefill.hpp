@@ -126,7 +126,10 @@ __device__ __forceinline__ int64_t prefill_items(const AttnArgs& a) { return pre
 // the sums are rescaled (fp32 sums and bf16 weights have the range).
 constexpr float PF_SLACK = 8.0f;
 
-template <int D, int NW>
+// LEAD: not the prompts of sequences, but the new tokens of a whole batch over the
+// prefix that its sequences share (attn_shared.hpp), each at its own position, in
+// parts that are left to k_attn_shared_join.
+template <int D, int NW, bool LEAD = false>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(AttnArgs a) {
   constexpr int TS = PrefillShape<D, NW>::TS, COLS = PrefillShape<D, NW>::COLS;
   constexpr int RING = PF_RING, KRING = PF_KRING, KS = D / 16, DT = D / 32, SUB = TS / 32;
@@ -144,17 +147,36 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   // the blocks of one stay on one XCD, whose L2 then holds its keys
   const int kvh = blockIdx.x % a.kv_heads, bi = blockIdx.x / a.kv_heads, split = bi / a.col_blocks;
   int b, cb;
-  if (!prefill_block<COLS>(a, bi - split * a.col_blocks, b, cb)) return;
-  const AttnSeq s = attn_seq(a, b);
+  AttnSeq s;
+  if constexpr (LEAD) {
+    b = 0;
+    cb = bi - split * a.col_blocks;
+    s = AttnSeq{0, a.B * a.n_q, a.shared, 0};
+  } else {
+    if (!prefill_block<COLS>(a, bi - split * a.col_blocks, b, cb)) return;
+    s = attn_seq(a, b);
+  }
   const int cols = s.n * a.group;
   const int c0 = cb * COLS;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, half = lane >> 5;
   const int w = uniform(tid >> 6);
   const int first = s.first;
-  const int p_first = uniform(first + c0 / a.group), p_last = uniform(first + (min(c0 + COLS, cols) - 1) / a.group);
-  AttnTiles tl = attn_tiles<TS>(a, p_first, p_last);
-  const bool whole = tl.n <= a.tiles_per_split;
-  if (!tl.keep_part(split, a.tiles_per_split)) return;
+  int p_first, p_last;
+  AttnTiles tl;
+  AttnSpan span{};
+  bool whole = false;
+  if constexpr (LEAD) {
+    span = attn_span(a, min(c0 + 32 * w + r, cols - 1), c0, min(c0 + COLS, cols));
+    p_first = min(span.first, a.shared - 1);
+    p_last = span.last;
+    tl = attn_tiles_between<TS>(a, 0, attn_window_lo(a, span.first), min(a.shared, p_last + 1));
+    if (!tl.keep_part(split, a.p_tiles_per_split)) tl.n = 0;
+  } else {
+    p_first = uniform(first + c0 / a.group), p_last = uniform(first + (min(c0 + COLS, cols) - 1) / a.group);
+    tl = attn_tiles<TS>(a, p_first, p_last);
+    whole = tl.n <= a.tiles_per_split;
+    if (!tl.keep_part(split, a.tiles_per_split)) return;
+  }
   const int last = scalar(tl.n - 1), skip = scalar(tl.skip), na = scalar(tl.na), jump = scalar(tl.b0 - tl.na);
   // first key of tile v of this part; past its end, of the last one
   auto key_of = [&](int v) __attribute__((always_inline)) {
@@ -183,8 +205,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qp + 16 * ks);
   }
   // of this wavefront's columns, the first position and the last window start
-  const int wp_first = uniform(first + min(c0 + 32 * w, cols - 1) / a.group);
-  const int wlo_last = attn_window_lo(a, uniform(first + min(c0 + 32 * w + 31, cols - 1) / a.group));
+  const int wp_first = LEAD ? p_first : uniform(first + min(c0 + 32 * w, cols - 1) / a.group);
+  const int wlo_last =
+      attn_window_lo(a, LEAD ? p_last : uniform(first + min(c0 + 32 * w + 31, cols - 1) / a.group));
 
   const int ps = 1 << a.page_shift;
   const uint32_t head_bytes = static_cast<uint32_t>(2 * D) << a.page_shift;
@@ -194,8 +217,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     for (int i = tid; i < TS / 16 * n; i += NW * 64) {
       const int v = first_tile + i / (TS / 16), part = i % (TS / 16);
       const int key = min(key_of(v) + 16 * part, s.len - 1);
-      ids[TS / 16 * (v & (PF_IDS - 1)) + part] =
-          min(max(a.page_table[b * a.max_pages + (key >> a.page_shift)], 0), a.n_pages - 1);
+      const int32_t page = LEAD ? a.shared_pages[key >> a.page_shift]
+                                : a.page_table[b * a.max_pages + (key >> a.page_shift)];
+      ids[TS / 16 * (v & (PF_IDS - 1)) + part] = min(max(page, 0), a.n_pages - 1);
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xC07F);          // the writes have been done (lgkmcnt 0)
@@ -265,8 +289,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   auto mask = [&](int v, f32x16 (&x)[SUB]) __attribute__((always_inline)) {
     const int key0 = key_of(v);
     if (key0 + TS - 1 <= wp_first && (key0 >= wlo_last || key0 + TS <= tl.sinks)) return;
-    const int pos = first + col / a.group;
-    const uint64_t see = visible_bits(key0 + 8 * half, pos, attn_window_lo(a, pos), tl.sinks);
+    const int pos = LEAD ? span.pos : first + col / a.group;
+    const uint64_t see =
+        visible_bits(key0 + 8 * half, LEAD ? min(pos, a.shared - 1) : pos, attn_window_lo(a, pos), tl.sinks);
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
@@ -438,9 +463,20 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   if (c0 + 32 * w + r >= cols) return;
   const int64_t row = row_of();
   if (!whole) {
-    const int64_t item = prefill_item(a, bi - split * a.col_blocks, kvh, 32 * w + r) + split, items = prefill_items(a);
-    if (half == 0) *reinterpret_cast<float2*>(a.ws + items * D + 2 * item) = float2{m, lt};
-    float* o = a.ws + item * D + 4 * half;
+    int64_t item;
+    float *sums, *ml;
+    if constexpr (LEAD) {
+      item = (static_cast<int64_t>(kvh) * cols + col) * a.p_splits + split;
+      sums = a.pws;
+      ml = a.pml;
+    } else {
+      item = prefill_item(a, bi - split * a.col_blocks, kvh, 32 * w + r) + split;
+      sums = a.ws;
+      ml = a.ws + prefill_items(a) * D;
+    }
+    if (half == 0) *reinterpret_cast<float2*>(ml + 2 * item) = float2{m, lt};
+    if (LEAD && last < 0) return;                // a part without keys has a sum of 0, and its values are not read
+    float* o = sums + item * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll

@@ -14,6 +14,7 @@
 #include "attn_decode.hpp"
 #include "attn_prefill.hpp"
 #include "attn_prepare.hpp"
+#include "attn_shared.hpp"
 
 namespace {
 
@@ -240,6 +241,115 @@ int decode(const AttnArgs& a, const DecodePlan& p, hipStream_t s) {
                            : launch(k_attn_join<D, 4>, grid, dim3(256), s, a);
 }
 
+AttnArgs attn_args(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t B, int64_t max_q,
+                   const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages, int64_t max_len, uint16_t* out,
+                   void* workspace) {
+  AttnArgs a{};
+  a.q = q;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.out = out;
+  a.seq_lens = seq_lens;
+  a.page_table = page_table;
+  a.ws = static_cast<float*>(workspace);
+  a.max_pages = max_pages;
+  a.n_pages = static_cast<int32_t>(cache->n_pages);
+  a.B = static_cast<int32_t>(B);
+  a.n_q = static_cast<int32_t>(max_q);
+  a.max_len = static_cast<int32_t>(max_len);
+  a.heads = c->n_heads;
+  a.kv_heads = c->n_kv_heads;
+  a.group = c->n_heads / c->n_kv_heads;
+  a.page_shift = page_shift_of(c->page_size);
+  a.window = static_cast<int32_t>(std::min<int64_t>(c->window, kMaxKeys));
+  a.sinks = static_cast<int32_t>(std::min<int64_t>(c->n_sinks, kMaxKeys));
+  a.scale_log2 = c->scale * 1.44269504088896340736f;
+  return a;
+}
+
+// How a decode call behind a shared prefix is cut: the prefix's tiles in parts for the columns of the whole batch,
+// and each sequence's own tiles in parts.
+struct SharedPlan {
+  bool wide;                         // the prefix in column blocks of k_attn_prefill, not of k_attn_decode
+  int p_splits, p_tiles_per_split, splits, tiles_per_split;
+  int col_blocks;                    // wide: of the prefix
+  bool again;                        // several blocks read the same keys
+  int64_t p_blocks, blocks;          // of the launches (not wide: p_blocks of the first ones of `blocks`)
+  int join_waves;
+  int64_t join_blocks;
+  int64_t p_items, items;            // columns times parts
+  size_t ws_bytes;
+};
+
+constexpr int64_t SHARED_WIDE = 64;  // columns of a key/value head from which the prefix is taken in wide blocks
+
+template <int D>
+SharedPlan shared_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len, int64_t shared) {
+  constexpr int NW = 4;
+  using S = PrefillShape<D, NW>;
+  SharedPlan p{};
+  const int64_t group = c->n_heads / c->n_kv_heads, cols = n_q * group, p_cols = B * cols, rows = p_cols * c->n_kv_heads;
+  int64_t tiles = cdiv(max_len, 32) - shared / 32;
+  if (c->window)
+    tiles = std::min(tiles, cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(std::max<int64_t>(c->n_sinks - shared, 0), 32) + 1);
+  const int64_t p_tiles = cdiv(shared, 32);
+  const int64_t col_blocks = cdiv(cols, 32), p_col_blocks = cdiv(p_cols, 32);
+  const int64_t places = 256 * attn_blocks_per_cu(D);
+  auto round = [](int64_t tps) {
+    tps = cdiv(tps, ATTN_NW) * ATTN_NW;
+    return tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
+  };
+  p.wide = p_cols > SHARED_WIDE;
+  const int64_t own = B * c->n_kv_heads * col_blocks * tiles, lead = p.wide ? 0 : c->n_kv_heads * p_col_blocks * p_tiles;
+  const int64_t tps = round(cdiv(own + lead, places));
+  p.tiles_per_split = static_cast<int>(tps);
+  p.splits = tiles > 0 ? static_cast<int>(cdiv(tiles, tps)) : 1;
+  p.blocks = B * c->n_kv_heads * p.splits;
+  if (col_blocks > 1) p.blocks = cdiv(p.blocks, 8) * 8 * col_blocks;
+  p.again = col_blocks > 1 || (!p.wide && p_col_blocks > 1);
+  if (p.wide) {
+    const int64_t wide_tiles = cdiv(shared, S::TS), busy = cdiv(p_cols, S::COLS) * c->n_kv_heads;
+    p.col_blocks = static_cast<int>(cdiv(p_cols, S::COLS));
+    const int64_t size = std::max(cdiv(busy * wide_tiles, 256 * S::PER_CU), PF_LEAST);
+    p.p_tiles_per_split = static_cast<int>(size);
+    p.p_splits = static_cast<int>(cdiv(wide_tiles, size));
+    p.p_blocks = busy * p.p_splits;
+  } else {
+    p.p_tiles_per_split = static_cast<int>(tps);
+    p.p_splits = static_cast<int>(cdiv(p_tiles, tps));
+    p.p_blocks = c->n_kv_heads * p.p_splits;
+    if (p_col_blocks > 1) p.p_blocks = cdiv(p.p_blocks, 8) * 8 * p_col_blocks;
+    p.blocks += p.p_blocks;
+  }
+  p.join_waves = rows < 1024 ? 4 : 1;            // as at k_attn_join
+  p.join_blocks = cdiv(rows, 4 / p.join_waves);
+  p.p_items = rows * p.p_splits;
+  p.items = rows * p.splits;
+  p.ws_bytes = size_t(p.p_items + p.items) * (D + 2) * 4;
+  return p;
+}
+
+int validate_shared(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len, int64_t shared) {
+  const int st = validate_sizes(c, 0, B, n_q, max_len, 0);
+  if (st) return st;
+  return shared < 0 || shared > max_len ? MOE_MLP_ERR_BAD_SHAPE : MOE_MLP_OK;
+}
+
+template <int D>
+int decode_shared(AttnArgs a, const SharedPlan& p, hipStream_t s) {
+  if (p.wide && p.p_splits) {
+    a.col_blocks = p.col_blocks;
+    const int st = launch(k_attn_prefill<D, 4, true>, dim3(static_cast<unsigned>(p.p_blocks)), dim3(256), s, a);
+    if (st) return st;
+  }
+  const int st = launch(p.again ? k_attn_decode<D, true, true> : k_attn_decode<D, false, true>,
+                        dim3(static_cast<unsigned>(p.blocks)), dim3(ATTN_NW * 64), s, a);
+  if (st) return st;
+  const dim3 grid(static_cast<unsigned>(p.join_blocks));
+  return p.join_waves == 1 ? launch(k_attn_shared_join<D, 1>, grid, dim3(256), s, a)
+                           : launch(k_attn_shared_join<D, 4>, grid, dim3(256), s, a);
+}
+
 int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint16_t* q, int64_t T, const int32_t* cu_q,
               int64_t B, int64_t max_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
               int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream, int prefill) {
@@ -257,28 +367,9 @@ int attention(const moe_attn_config* c, const moe_attn_cache* cache, const uint1
       !aligned(cu_q, 4))
     return MOE_MLP_ERR_MISALIGNED;
   if (ws_bytes < need) return MOE_MLP_ERR_WORKSPACE_TOO_SMALL;
-  AttnArgs a{};
-  a.q = q;
-  a.k = cache->k;
-  a.v = cache->v;
-  a.out = out;
-  a.seq_lens = seq_lens;
-  a.page_table = page_table;
+  AttnArgs a = attn_args(c, cache, q, B, max_q, seq_lens, page_table, max_pages, max_len, out, workspace);
   a.cu_q = prefill ? cu_q : nullptr;
-  a.ws = static_cast<float*>(workspace);
   a.T = T;
-  a.max_pages = max_pages;
-  a.n_pages = static_cast<int32_t>(cache->n_pages);
-  a.B = static_cast<int32_t>(B);
-  a.n_q = static_cast<int32_t>(max_q);
-  a.max_len = static_cast<int32_t>(max_len);
-  a.heads = c->n_heads;
-  a.kv_heads = c->n_kv_heads;
-  a.group = c->n_heads / c->n_kv_heads;
-  a.page_shift = page_shift_of(c->page_size);
-  a.window = static_cast<int32_t>(std::min<int64_t>(c->window, kMaxKeys));
-  a.sinks = static_cast<int32_t>(std::min<int64_t>(c->n_sinks, kMaxKeys));
-  a.scale_log2 = c->scale * 1.44269504088896340736f;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!prefill) {
     const DecodePlan p = decode_plan(c, B, max_q, max_len);
@@ -407,6 +498,57 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
                     int64_t max_len, uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
   return attention(cfg, cache, q, 0, nullptr, B, n_q, seq_lens, page_table, max_pages, max_len, out, workspace,
                    ws_bytes, stream, 0);
+}
+
+int moe_attn_shared_workspace_size(const moe_attn_config* cfg, int64_t B, int64_t n_q, int64_t max_len,
+                                   int64_t shared_len, size_t* bytes) {
+  const int st = validate_shared(cfg, B, n_q, max_len, shared_len);
+  if (st) return st;
+  if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = 0;
+  if (B == 0) return MOE_MLP_OK;
+  return with_dim(cfg->head_dim, [&](auto dc) -> int {
+    const SharedPlan p = shared_plan<decltype(dc)::value>(cfg, B, n_q, max_len, shared_len);
+    if (std::max({p.blocks, p.p_blocks, p.join_blocks}) >= kMaxThreads / 256) return MOE_MLP_ERR_BAD_SHAPE;
+    *bytes = p.ws_bytes;
+    return MOE_MLP_OK;
+  });
+}
+
+int moe_attn_decode_shared(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,
+                           int64_t n_q, const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages,
+                           int64_t max_len, const int32_t* shared_pages, int64_t shared_len, uint16_t* out,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  int st = moe_attn_shared_workspace_size(cfg, B, n_q, max_len, shared_len, &need);
+  if (st) return st;
+  if (max_pages < 0 || max_pages >= kInt32End || max_len > max_pages * cfg->page_size) return MOE_MLP_ERR_BAD_SHAPE;
+  if (B == 0) return MOE_MLP_OK;
+  st = validate_cache(cfg, cache);
+  if (st) return st;
+  if (!q || !out || !seq_lens || (max_len > 0 && !page_table) || (shared_len > 0 && !shared_pages) || !workspace)
+    return MOE_MLP_ERR_NULL_ARG;
+  if (!aligned(q) || !aligned(out) || !aligned(workspace) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
+      !aligned(shared_pages, 4))
+    return MOE_MLP_ERR_MISALIGNED;
+  if (ws_bytes < need) return MOE_MLP_ERR_WORKSPACE_TOO_SMALL;
+  AttnArgs a = attn_args(cfg, cache, q, B, n_q, seq_lens, page_table, max_pages, max_len, out, workspace);
+  a.T = B * n_q;
+  a.shared_pages = shared_pages;
+  a.shared = static_cast<int32_t>(shared_len);
+  return with_dim(cfg->head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    const SharedPlan p = shared_plan<D>(cfg, B, n_q, max_len, shared_len);
+    a.splits = p.splits;
+    a.tiles_per_split = p.tiles_per_split;
+    a.p_splits = p.p_splits;
+    a.p_tiles_per_split = p.p_tiles_per_split;
+    a.p_blocks = p.wide ? 0 : static_cast<int32_t>(p.p_blocks);
+    a.pws = a.ws + p.items * D;
+    a.ml = a.pws + p.p_items * D;
+    a.pml = a.ml + p.items * 2;
+    return decode_shared<D>(a, p, static_cast<hipStream_t>(stream));
+  });
 }
 
 int moe_attn_prefill(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t T,
