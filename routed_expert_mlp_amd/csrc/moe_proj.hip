@@ -46,6 +46,37 @@ int norm(const NormArgs& a, hipStream_t s) {
   return launch(k_proj_norm<WPR, 4>, grid, block, s, a);
 }
 
+template <int NT, int MT, int U>
+int fp8_few(const Fp8Args& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(cdiv(a.N, 16 * NT) * cdiv(a.T, 16 * MT)));
+  return launch(k_proj_fp8_few<NT, MT, 8, U>, grid, dim3(512), s, a);
+}
+
+template <int WN, int WT, int TT>
+int fp8_tile(const Fp8Args& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(cdiv(cdiv(a.N, 64 * WN) * cdiv(a.T, 16 * TT * WT), 8) * 8));
+  return launch(k_proj_fp8_tile<WN, WT, 4, TT>, grid, dim3(64 * WN * WT), s, a);
+}
+
+// The smallest blocks that the 256 CUs take at once, one each, since the reads of a
+// block do not get shorter when it is one of more (4096 columns; blocks of 16 x 16,
+// 32 x 16, 32 x 64, 64 x 64 outputs x tokens without LDS, 128 x 128 tiles):
+//   1 token to 4096: 6.0, 6.8 us; to 6144: 8.3, 7.1 us;
+//   32 to 1024: 6.2, 8.8, 11.6 us; 48 to 6144: -, -, 13.8, 18.4, 23.4 us;
+//   128 to 6144: -, -, 28.1, 20.3, 24.5 us; 700 to 1536: -, -, 39, 38, 24.5 us.
+// Past that, tiles of 128 x 128 while their blocks, two a CU, have places at once, and
+// of 256 x 256 then (2048 to 4096: 39 and 52 us; 1536 to 6144: 58 and 53 us).  Up to 16
+// tokens the weights' stream is all there is, however long.
+int fp8(const Fp8Args& a, hipStream_t s) {
+  auto blocks = [&](int n, int t) { return cdiv(a.N, n) * cdiv(a.T, t); };
+  if (blocks(16, 16) <= 256) return fp8_few<1, 1, 4>(a, s);
+  if (a.T <= 16 || blocks(32, 16) <= 256) return fp8_few<2, 1, 2>(a, s);
+  if (blocks(32, 64) <= 256) return fp8_few<2, 4, 2>(a, s);
+  if (blocks(64, 64) <= 256) return fp8_few<4, 4, 1>(a, s);
+  if (blocks(128, 128) <= 512) return fp8_tile<2, 2, 4>(a, s);
+  return fp8_tile<4, 2, 8>(a, s);
+}
+
 // How the adapters' products are cut.
 struct LoraPlan {
   int64_t windows, parts, part_chunks;
@@ -140,11 +171,7 @@ int moe_proj_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const
   a.T = T;
   a.N = static_cast<int32_t>(N);
   a.K = static_cast<int32_t>(K);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const unsigned blocks = static_cast<unsigned>(N / 16 * cdiv(T, 64));
-  if (T <= 16) return launch(k_proj_fp8_few<1, 8>, dim3(blocks), dim3(512), s, a);
-  if (T <= 32) return launch(k_proj_fp8_few<2, 8>, dim3(blocks), dim3(512), s, a);
-  return launch(k_proj_fp8_few<4, 8>, dim3(blocks), dim3(512), s, a);
+  return fp8(a, static_cast<hipStream_t>(stream));
 }
 
 int moe_proj_lora_workspace_size(const moe_proj_adapters* adapters, int64_t T, size_t* bytes) {

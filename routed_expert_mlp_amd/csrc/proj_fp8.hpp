@@ -21,6 +21,7 @@
 
 namespace moe {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 struct Fp8Args {
@@ -35,63 +36,279 @@ struct Fp8Args {
 
 // C += A B over 128 columns: lane l holds 32 of the 128 of row (column) l % 16 of
 // A (B), the same ones in both, and rows 4 (l / 16) .. +3 of column l % 16 of C.
-__device__ __forceinline__ f32x4 mfma_e4m3(uint4 a0, uint4 a1, uint4 b0, uint4 b1, f32x4 c) {
-  const i32x8 a = {static_cast<int>(a0.x), static_cast<int>(a0.y), static_cast<int>(a0.z), static_cast<int>(a0.w),
-                   static_cast<int>(a1.x), static_cast<int>(a1.y), static_cast<int>(a1.z), static_cast<int>(a1.w)};
-  const i32x8 b = {static_cast<int>(b0.x), static_cast<int>(b0.y), static_cast<int>(b0.z), static_cast<int>(b0.w),
-                   static_cast<int>(b1.x), static_cast<int>(b1.y), static_cast<int>(b1.z), static_cast<int>(b1.w)};
+__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
-// Few tokens: a block takes 16 rows of the weights and 16 MT tokens, its NW
-// wavefronts every NW'th span, straight from memory into the operand registers,
-// and they join in LDS.
-template <int MT, int NW>
+// Two pieces of 16 bytes as an operand.
+__device__ __forceinline__ i32x8 operand(const uint4* p, const uint4* q) {
+  const i32x4 a = *reinterpret_cast<const i32x4*>(p), b = *reinterpret_cast<const i32x4*>(q);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Few tokens, or few outputs: a block takes 16 NT rows of the weights and 16 MT
+// tokens, its NW wavefronts every NW'th span, straight from memory into the operand
+// registers, U spans at a time in flight; they join in LDS, pair by pair.
+// What bounds it: the weights' stream with a token (4096 columns to 6144: 7 us, 3.6
+// TB/s with the launch in it), with more the reads of the tokens' rows, which every
+// block takes from L2 again: 48 tokens 14 us, 517 tokens to 576 columns 15.5 us.
+// The scales of four spans come in one load: a load of 16 rows' scales takes as long
+// as one of 16 bytes of each (517 tokens: 17.6 us with a load a span).
+template <int NT, int MT, int NW, int U>
 __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rows = a.N >> 4, n0 = blockIdx.x % rows * 16, spans = a.K >> 7;
+  const int rows = (a.N + 16 * NT - 1) / (16 * NT), n0 = static_cast<int>(blockIdx.x % rows) * (16 * NT), spans = a.K >> 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / rows) * (16 * MT);
-  const uint8_t* const wp = a.w + static_cast<int64_t>(n0 + c) * a.K + 16 * g;
   const float* const ws = a.ws + static_cast<int64_t>(n0 >> 7) * spans;
+  const uint8_t* wp[NT];
   const uint8_t* xp[MT];
   const float* xs[MT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) wp[n] = a.w + static_cast<int64_t>(min(n0 + 16 * n + c, a.N - 1)) * a.K + 16 * g;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int64_t t = min(t0 + 16 * m + c, a.T - 1);
     xp[m] = a.x + t * a.K + 16 * g;
     xs[m] = a.xs + t * spans;
   }
-  f32x4 acc[MT];
+  f32x4 acc[NT][MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4{};
-  for (int s = w; s < spans; s += NW) {
-    const uint4 w0 = *reinterpret_cast<const uint4*>(wp + 128 * s);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(wp + 128 * s + 64);
-    const float wscale = ws[s];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const uint4 x0 = *reinterpret_cast<const uint4*>(xp[m] + 128 * s);
-      const uint4 x1 = *reinterpret_cast<const uint4*>(xp[m] + 128 * s + 64);
-      const float scale = wscale * xs[m][s];
-      const f32x4 p = mfma_e4m3(w0, w1, x0, x1, f32x4{});
+    for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{};
+  for (int s4 = w; s4 < spans; s4 += NW * 4) {
+    // scales of four spans in one load a token tile, span s4 + NW g in lanes (g, token); 0 past the end
+    float sc[MT];
+    const int sg = s4 + NW * g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(p[i], scale, acc[m][i]);
+    for (int m = 0; m < MT; ++m) sc[m] = sg < spans ? xs[m][min(sg, spans - 1)] * ws[min(sg, spans - 1)] : 0.0f;
+#pragma unroll
+    for (int u0 = 0; u0 < 4; u0 += U) {
+      if (u0 && s4 + NW * u0 >= spans) continue;
+      i32x8 wf[U][NT], xf[U][MT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s = min(s4 + NW * (u0 + u), spans - 1);    // past the end the last span, with scales of 0
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4* const r = reinterpret_cast<const uint4*>(wp[n] + 128 * s);
+          wf[u][n] = operand(r, r + 4);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4* const r = reinterpret_cast<const uint4*>(xp[m] + 128 * s);
+          xf[u][m] = operand(r, r + 4);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float f = __shfl(sc[m], 16 * (u0 + u) + c);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const f32x4 p = mfma_e4m3(wf[u][n], xf[u][m], f32x4{});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[i], f, acc[n][m][i]);
+          }
+        }
     }
   }
-  __shared__ f32x4 part[NW][MT][64];
+  __shared__ f32x4 part[NW / 2][NT][MT][64];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) part[w][m][lane] = acc[m];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MT * 64; i += NW * 64) {
-    const int m = i >> 6, l = i & 63;
-    f32x4 sum = part[0][m][l];
+  for (int step = NW / 2; step; step >>= 1) {
+    if (step < NW / 2) __syncthreads();
+    if (w >= step && w < 2 * step) {
 #pragma unroll
-    for (int j = 1; j < NW; ++j) sum += part[j][m][l];
-    const int64_t t = t0 + 16 * m + (l & 15);
-    if (t < a.T)
-      *reinterpret_cast<uint2*>(a.y + t * a.N + n0 + 4 * (l >> 4)) =
-          uint2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) part[w - step][n][m][lane] = acc[n][m];
+    }
+    __syncthreads();
+    if (w < step) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] += part[w][n][m][lane];
+    }
+  }
+  if (w) return;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n0 + 16 * n >= a.N) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int64_t t = t0 + 16 * m + c;
+      const f32x4 v = acc[n][m];
+      if (t < a.T)
+        *reinterpret_cast<uint2*>(a.y + t * a.N + n0 + 16 * n + 4 * g) =
+            uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+  }
+}
+
+// Many tokens: tiles of 16 NJ WN weight rows x 16 TT WT tokens, one a block of
+// WN x WT wavefronts with 16 NJ x 16 TT each.  Spans of both operands go to LDS by
+// DMA, two slots.
+//   * A slot's row has 8 pieces of 16 bytes; piece p of row r is at place p ^ (r & 7),
+//     so that the 16 rows of a fragment, 128 bytes apart, fall to different banks.
+//   * Each 64 weight rows are in the order in which a lane ends with 16 neighbouring
+//     outputs of its token: row 16 j + 4 g + i of the slot is weight row
+//     16 g + 4 j + i, and lane (g, token) has elements i of tiles j.
+//   * The scales of the tokens come in groups of 4 spans, 64 tokens a transfer (a load
+//     of its own by each wavefront for each span: 184 us where this took 117).
+//   * There is one barrier a span; the next span's transfers are spread over the
+//     products behind it.  (A barrier before the last products, which then hide the
+//     reads of the next span's first fragments: no faster, for 20 registers more.)
+//   * Transfers past the last row bring zeros (bounds of the buffer).
+// Measured, 4096 tokens of 4096 columns to 6144: 117-125 us in tiles of 256 x 256,
+// 1.65-1.76 PFLOP/s, where a large library product of E4M3 with one scale in all
+// reaches 2.3 (this size) to 3.0.  The chip is at its power limit then: without the
+// transfers and the scales it takes 90 us with all CUs and 35 us a round with nine,
+// not twice as long.  The fmas take 9% of the time, the transfers 13%, the reads of
+// LDS 25%.  Wavefronts of 128 x 128, one a SIMD, do not keep the matrix unit busy
+// (163 us); instructions of 32 x 32 over half a span need more registers for the
+// sums of a span (131-139 us).
+template <int WN, int WT, int NJ, int TT>
+__global__ __launch_bounds__(64 * WN * WT, WN * WT > 4 || NJ * TT <= 16 ? 2 : 1) void k_proj_fp8_tile(Fp8Args a) {
+  constexpr int NW = WN * WT, BN = 16 * NJ * WN, BT = 16 * TT * WT;
+  constexpr int IW = BN * 8 / 64 / NW, IX = BT * 8 / 64 / NW;     // transfers of a wavefront a span
+  constexpr int SPREAD = 4, LAG = 3;                         // products between one and its fmas
+  static_assert(BN * 8 % (64 * NW) == 0 && BT * 8 % (64 * NW) == 0, "whole transfers");
+  static_assert(BT % 64 == 0 && BT / 64 <= NW, "scales: 64 tokens a wavefront");
+  __shared__ uint4 w0[BN * 8], w1[BN * 8], x0[BT * 8], x1[BT * 8], xsl[2 * BT];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wv % WN, wt = wv / WN;
+  const int n_tiles = (a.N + BN - 1) / BN, spans = a.K >> 7;
+  // an XCD (every eighth block) has neighbouring tiles, GT tokens' tiles high, whose operands its L2 shares
+  const int t_tiles = static_cast<int>((a.T + BT - 1) / BT), total = n_tiles * t_tiles;
+  const int id = static_cast<int>(blockIdx.x & 7) * ((total + 7) >> 3) + static_cast<int>(blockIdx.x >> 3);
+  if (id >= total) return;
+  constexpr int GT = 4;
+  const int group = id / (GT * n_tiles), high = min(GT, t_tiles - group * GT), in = id - group * GT * n_tiles;
+  const int n0 = in / high * BN;
+  const int64_t t0 = static_cast<int64_t>(group * GT + in % high) * BT;
+  using lds_t = void __attribute__((address_space(3)));
+  const uint8_t* const wbase = a.w + static_cast<int64_t>(n0) * a.K;
+  const uint8_t* const xbase = a.x + t0 * a.K;
+  const float* const sbase = a.xs + t0 * spans;
+  const uint32_t rows = static_cast<uint32_t>(a.T - t0 < BT ? a.T - t0 : BT);
+  const uint32_t wbytes = static_cast<uint32_t>(min(a.N - n0, BN)) * a.K, xbytes = rows * a.K, sbytes = rows * spans * 4;
+  auto bring = [&](const void* base, uint32_t bytes, int off, int step, uint4* dst) __attribute__((always_inline)) {
+    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_t*)dst, 16, off, step, 0, 0);
+  };
+  // this lane's piece of transfer i: row (i NW + wv) 8 + lane / 8 of the slot
+  int woff[IW], xoff[IX];
+#pragma unroll
+  for (int i = 0; i < IW; ++i) {
+    const int r = (i * NW + wv) * 8 + (lane >> 3), m = r & 15, j = (r >> 4) & 3;
+    woff[i] = ((r & ~63) + 16 * (m >> 2) + 4 * j + (m & 3)) * a.K + 16 * ((lane & 7) ^ (r & 7));
+  }
+#pragma unroll
+  for (int i = 0; i < IX; ++i) {
+    const int r = (i * NW + wv) * 8 + (lane >> 3);
+    xoff[i] = r * a.K + 16 * ((lane & 7) ^ (r & 7));
+  }
+  auto issue_one = [&](int s, uint4* ws, uint4* xs, int i) __attribute__((always_inline)) {
+    if (i < IW) bring(wbase, wbytes, woff[i], 128 * s, ws + (i * NW + wv) * 64);
+    else bring(xbase, xbytes, xoff[i - IW], 128 * s, xs + ((i - IW) * NW + wv) * 64);
+  };
+  auto issue = [&](int s, uint4* ws, uint4* xs) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < IW + IX; ++i) issue_one(s, ws, xs, i);
+  };
+  // scales: of the tokens, group q (spans 4 q .. 4 q + 3), and of the wavefront's rows
+  auto issue_scales = [&](int q) __attribute__((always_inline)) {
+    if (wv < BT / 64) bring(sbase, sbytes, (64 * wv + lane) * spans * 4, 16 * q, xsl + (q & 1) * BT + 64 * wv);
+  };
+  const float* const wscale = a.ws + static_cast<int64_t>(min(n0 + 16 * NJ * wn, a.N - 1) >> 7) * spans;
+  // this wavefront's transfers have come, and everyone is here
+  auto arrive = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  const int p0 = g ^ (c & 7), p1 = (g + 4) ^ (c & 7);
+  i32x8 wf[NJ], xf[2];
+  float scale[TT];
+  auto read_w = [&](const uint4* slot, int j) __attribute__((always_inline)) {
+    const uint4* row = slot + (16 * NJ * wn + 16 * j + c) * 8;
+    wf[j] = operand(row + p0, row + p1);
+  };
+  auto read_x = [&](const uint4* slot, int t) __attribute__((always_inline)) {
+    const uint4* row = slot + (16 * (TT * wt + t) + c) * 8;
+    xf[t & 1] = operand(row + p0, row + p1);
+  };
+  auto read_scale = [&](int s, int t) __attribute__((always_inline)) {
+    return reinterpret_cast<const float*>(xsl)[((s >> 2 & 1) * BT + 16 * (TT * wt + t) + c) * 4 + (s & 3)];
+  };
+  f32x4 acc[TT][NJ], part[LAG + 1];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[t][j] = f32x4{};
+  auto add = [&](int m) __attribute__((always_inline)) {
+    const int t = m / NJ, j = m % NJ;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(part[m % (LAG + 1)][i], scale[t], acc[t][j][i]);
+    asm volatile("" : "+v"(acc[t][j]));          // here, beside the matrix instructions, and not behind the branch
+  };
+  float ws = wscale[0];
+  // span s of slots wl and xl; the next one goes to the others
+  auto span = [&](int s, const uint4* wl, const uint4* xl, uint4* wnext, uint4* xnext) __attribute__((always_inline)) {
+    constexpr int M = NJ * TT, I = IW + IX, SP = M / SPREAD;
+    arrive();
+    const int next = min(s + 1, spans - 1);      // past the end the last span again, which nobody reads
+    read_x(xl, 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) read_w(wl, j);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) scale[t] = read_scale(s, t) * ws;
+    ws = wscale[next];                           // ahead of the transfers, so that nothing waits for those
+    if ((s & 3) == 0) issue_scales((s >> 2) + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int t = m / NJ, j = m % NJ;
+      if (j == 0 && t + 1 < TT) read_x(xl, t + 1);
+      part[m % (LAG + 1)] = mfma_e4m3(wf[j], xf[t & 1], f32x4{});
+      if (m >= LAG) add(m - LAG);
+#pragma unroll
+      for (int k = m * I / SP; k < (m + 1) * I / SP; ++k)
+        if (k < I) issue_one(next, wnext, xnext, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int m = M - LAG; m < M; ++m) add(m);
+  };
+  issue(0, w0, x0);
+  issue_scales(0);
+  int s = 0;
+  for (; s + 1 < spans; s += 2) {
+    span(s, w0, x0, w1, x1);
+    span(s + 1, w1, x1, w0, x0);
+  }
+  if (s < spans) span(s, w0, x0, w1, x1);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));      // transfers end before the block gives up its LDS
+#pragma unroll
+  for (int q = 0; q < NJ / 4; ++q) {
+    const int n = n0 + 16 * NJ * wn + 64 * q + 16 * g;
+    if (n >= a.N) return;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int64_t row = t0 + 16 * (TT * wt + t) + c;
+      if (row >= a.T) continue;
+      uint16_t* y = a.y + row * a.N + n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 u = acc[t][4 * q + 2 * h], v = acc[t][4 * q + 2 * h + 1];
+        *reinterpret_cast<uint4*>(y + 8 * h) = uint4{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                                                     pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+    }
   }
 }
 
