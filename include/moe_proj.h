@@ -18,7 +18,7 @@
  *     the default stream) of the current device and the call returns without
  *     waiting; calls can be captured into a HIP graph;
  *   - results are deterministic: no atomics, fixed summation orders.
- * Status codes are those of moe_mlp.h.  A call has T < 2^23 tokens; T == 0 is
+ * Status codes are those of moe_mlp.h.  A call has T < 2^22 tokens; T == 0 is
  * a no-op returning MOE_MLP_OK.
  */
 #ifndef MOE_PROJ_H

@@ -53,7 +53,7 @@ def test_library_exports_every_declared_function():
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 23), capi.ERR_BAD_SHAPE), (dict(H=0), capi.ERR_BAD_SHAPE),
+    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 22), capi.ERR_BAD_SHAPE), (dict(H=0), capi.ERR_BAD_SHAPE),
     (dict(H=4), capi.ERR_BAD_SHAPE), (dict(H=252), capi.ERR_BAD_SHAPE), (dict(H=-8), capi.ERR_BAD_SHAPE),
     (dict(H=16392, stride=16392), capi.ERR_BAD_SHAPE), (dict(stride=248), capi.ERR_BAD_SHAPE),
     (dict(stride=260), capi.ERR_BAD_SHAPE), (dict(stride=1 << 31), capi.ERR_BAD_SHAPE),
@@ -73,7 +73,7 @@ def test_norm_refusals(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 23), capi.ERR_BAD_SHAPE), (dict(N=0), capi.ERR_BAD_SHAPE),
+    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 22), capi.ERR_BAD_SHAPE), (dict(N=0), capi.ERR_BAD_SHAPE),
     (dict(N=8), capi.ERR_BAD_SHAPE), (dict(N=72), capi.ERR_BAD_SHAPE), (dict(N=1 << 20), capi.ERR_BAD_SHAPE),
     (dict(K=0), capi.ERR_BAD_SHAPE), (dict(K=64), capi.ERR_BAD_SHAPE), (dict(K=1 << 20), capi.ERR_BAD_SHAPE),
     (dict(T=1 << 20, N=1 << 12), capi.ERR_BAD_SHAPE), (dict(N=-16), capi.ERR_BAD_SHAPE), (dict(K=-128), capi.ERR_BAD_SHAPE),
@@ -100,7 +100,7 @@ def test_adapter_refusals(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 23), capi.ERR_BAD_SHAPE), (dict(xs=56), capi.ERR_BAD_SHAPE),
+    (dict(T=-1), capi.ERR_BAD_SHAPE), (dict(T=1 << 22), capi.ERR_BAD_SHAPE), (dict(xs=56), capi.ERR_BAD_SHAPE),
     (dict(xs=68), capi.ERR_BAD_SHAPE), (dict(bs=40), capi.ERR_BAD_SHAPE), (dict(os=52), capi.ERR_BAD_SHAPE),
     (dict(os=1 << 31), capi.ERR_BAD_SHAPE), (dict(x=None), capi.ERR_NULL_ARG), (dict(ids=None), capi.ERR_NULL_ARG),
     (dict(base=None), capi.ERR_NULL_ARG), (dict(out=None), capi.ERR_NULL_ARG), (dict(ws=None), capi.ERR_NULL_ARG),
@@ -127,7 +127,7 @@ def test_lora_null_descriptor_and_weights():
                                 dict(in_features=(1 << 20) - 8, out_features=8, max_rank=256, n_adapters=1 << 20)])
 def test_lora_workspace_serves_fewer_tokens(kw):
     d, last = adapters(**kw), 0
-    for T in list(range(0, 200)) + [511, 512, 513, 4096, 32767, 32768, 32769, 40000, 1 << 20, (1 << 23) - 1]:
+    for T in list(range(0, 200)) + [511, 512, 513, 4096, 32767, 32768, 32769, 40000, 1 << 20, (1 << 22) - 1]:
         st, n = size(d, T)
         assert st == 0 and n >= last, T
         last = n
