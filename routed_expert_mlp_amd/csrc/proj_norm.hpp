@@ -76,6 +76,7 @@ struct E4m3Block {
   float p[8], e[8];          // |h w| = |p + e|
   float top, rest;           // the largest of the block, and what is left over of it
   __device__ __forceinline__ void products(const float (&h)[8], const float (&w)[8]) {
+#pragma clang fp contract(off)
     top = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -92,6 +93,7 @@ struct E4m3Block {
   }
   // s: the scale.
   __device__ __forceinline__ uint2 codes(float inv, float s) const {
+#pragma clang fp contract(off)       // the products below are rounded where it says so
     float z[8];
     if (top >= 0x1p-60f && top <= 0x1p100f && s > 1.17549435e-38f) {
       const float one = __builtin_amdgcn_rcpf(top), r = 448.0f * one;
