@@ -25,9 +25,9 @@ bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr
 // hipLaunchKernel says whether this launch failed; an error that an earlier
 // call of the process left behind is not taken for it.
 template <typename A>
-int launch(void (*kernel)(A), dim3 grid, dim3 block, hipStream_t s, A args) {
+int launch(void (*kernel)(A), dim3 grid, dim3 block, hipStream_t s, A args, size_t lds = 0) {
   void* p[] = {&args};
-  if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, p, 0, s) == hipSuccess)
+  if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, p, lds, s) == hipSuccess)
     return MOE_MLP_OK;
   (void)hipGetLastError();
   return MOE_MLP_ERR_HIP;
@@ -79,31 +79,42 @@ int fp8(const Fp8Args& a, hipStream_t s) {
 
 // How the adapters' products are cut.
 struct LoraPlan {
-  int64_t windows, parts, part_chunks;
+  bool grouped;                      // by k_lora_group
+  int64_t parts, part_chunks, down_x, up_x;
   int slots_down, slots_up, groups, col_blocks;
-  size_t ws_bytes;
+  size_t tiles_at, count_at, order_at, ws_bytes;     // in the workspace, behind v
 };
 
-// Parts of the sum over the input that fill the GPU with windows of 64 tokens; none shorter than a chunk for each
-// wavefront of a block.
-int64_t lora_parts(int64_t windows, int64_t chunks) {
-  return std::max<int64_t>(1, std::min(cdiv(chunks, 4), 512 / windows));
-}
+constexpr int64_t LORA_BLOCKS = 256;      // blocks of k_lora_down with something to do
 
 LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
   LoraPlan p{};
-  const int64_t chunks = cdiv(d->in_features, 64);
-  p.windows = cdiv(T, LORA_WINDOW);
-  p.part_chunks = cdiv(chunks, lora_parts(p.windows, chunks));
+  const int64_t chunks = cdiv(d->in_features, 64), vr = cdiv(d->max_rank, 16) * 16;
+  // parts of the sum over the input, for tiles of 64 tokens; none shorter than a chunk for each wavefront of a block
+  const int64_t most_parts = cdiv(chunks, LORA_DOWN);
+  p.part_chunks = cdiv(chunks, std::max<int64_t>(1, std::min(most_parts, LORA_BLOCKS / cdiv(T, 64))));
   p.parts = cdiv(chunks, p.part_chunks);
   p.groups = static_cast<int>(cdiv(d->max_rank, 16 * LORA_RT));
-  p.col_blocks = static_cast<int>(cdiv(d->out_features, 256));
-  const int64_t most = std::min<int64_t>(std::min<int64_t>(LORA_WINDOW, T), d->n_adapters);
-  p.slots_down = static_cast<int>(std::max<int64_t>(1, std::min(most, 1024 / p.windows)));
-  p.slots_up = static_cast<int>(std::max<int64_t>(1, std::min(most, 2048 / (p.windows * p.col_blocks))));
-  // of T tokens or fewer: parts are at most ceil(chunks / 4), and more than one only while parts x windows <= 512
-  const int64_t rows = std::min(T * cdiv(chunks, 4), std::max<int64_t>(T, 512 * LORA_WINDOW));
-  p.ws_bytes = size_t(rows) * (cdiv(d->max_rank, 16) * 16) * 4;
+  p.col_blocks = static_cast<int>(cdiv(d->out_features, 64 * LORA_UP));
+  p.grouped = T > 64 && d->n_adapters < LORA_BINS;
+  // every adapter, and the tokens without one, leave at most one tile unfilled
+  const int64_t tiles = T / 64 + std::min(T, d->n_adapters + 1);
+  if (p.grouped) {
+    p.down_x = p.up_x = tiles;
+  } else {
+    const int64_t windows = cdiv(T, 64), most = std::min(std::min<int64_t>(64, T), d->n_adapters);
+    auto slots = [&](int64_t blocks) { return static_cast<int>(std::max<int64_t>(1, std::min(most, blocks))); };
+    p.slots_down = slots(2048 / (windows * p.parts));
+    p.slots_up = slots(4096 / (windows * p.col_blocks));
+    p.down_x = windows * p.slots_down;
+    p.up_x = windows * p.slots_up;
+  }
+  // of T tokens or fewer: more than one part only while parts x tiles of 64 tokens are at most LORA_BLOCKS
+  const int64_t rows = std::min(T * most_parts, std::max<int64_t>(T, LORA_BLOCKS * 64));
+  p.tiles_at = size_t(rows) * vr * 4;
+  p.count_at = p.tiles_at + size_t(tiles) * 16;
+  p.order_at = p.count_at + 16;
+  p.ws_bytes = p.order_at + size_t(T) * 4;
   return p;
 }
 
@@ -224,13 +235,22 @@ int moe_proj_lora(const moe_proj_adapters* adapters, const uint16_t* x, int64_t 
   a.parts = static_cast<int32_t>(p.parts);
   a.part_chunks = static_cast<int32_t>(p.part_chunks);
   hipStream_t s = static_cast<hipStream_t>(stream);
+  char* const ws = static_cast<char*>(workspace);
+  a.tiles = reinterpret_cast<int4*>(ws + p.tiles_at);
+  a.n_tiles = reinterpret_cast<int32_t*>(ws + p.count_at);
+  a.order = reinterpret_cast<int32_t*>(ws + p.order_at);
+  if (p.grouped) {
+    const int sg = launch(k_lora_group, dim3(1), dim3(64 * LORA_GROUP), s, a);
+    if (sg) return sg;
+  }
   a.slots = p.slots_down;
-  const int sd = launch(k_lora_down, dim3(static_cast<unsigned>(p.windows * p.slots_down), static_cast<unsigned>(p.parts),
-                                          static_cast<unsigned>(p.groups)), dim3(256), s, a);
+  const dim3 down(static_cast<unsigned>(p.down_x), static_cast<unsigned>(p.parts), static_cast<unsigned>(p.groups));
+  const int sd = launch(p.grouped ? k_lora_down<true> : k_lora_down<false>, down, dim3(64 * LORA_DOWN), s, a);
   if (sd) return sd;
   a.slots = p.slots_up;
-  return launch(k_lora_up, dim3(static_cast<unsigned>(p.windows * p.slots_up), static_cast<unsigned>(p.col_blocks)),
-                dim3(256), s, a);
+  return launch(p.grouped ? k_lora_up<true> : k_lora_up<false>,
+                dim3(static_cast<unsigned>(p.up_x), static_cast<unsigned>(p.col_blocks)), dim3(64 * LORA_UP), s, a,
+                size_t(2 * 64) * (a.vr / 8 + 1) * 16);
 }
 
 }  // extern "C"
