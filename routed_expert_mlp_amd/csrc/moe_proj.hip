@@ -90,8 +90,8 @@ constexpr int64_t LORA_BLOCKS = 256;      // blocks of k_lora_down with somethin
 LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
   LoraPlan p{};
   const int64_t chunks = cdiv(d->in_features, 64), vr = cdiv(d->max_rank, 16) * 16;
-  // parts of the sum over the input, for tiles of 64 tokens; none shorter than a chunk for each wavefront of a block
-  const int64_t most_parts = cdiv(chunks, LORA_DOWN);
+  // parts of the sum over the input, for tiles of 64 tokens; none shorter than 8 chunks of 64 columns
+  const int64_t most_parts = cdiv(chunks, 8);
   p.part_chunks = cdiv(chunks, std::max<int64_t>(1, std::min(most_parts, LORA_BLOCKS / cdiv(T, 64))));
   p.parts = cdiv(chunks, p.part_chunks);
   p.groups = static_cast<int>(cdiv(d->max_rank, 16 * LORA_RT));
@@ -102,7 +102,7 @@ LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
   if (p.grouped) {
     p.down_x = p.up_x = tiles;
   } else {
-    const int64_t windows = cdiv(T, 64), most = std::min(std::min<int64_t>(64, T), d->n_adapters);
+    const int64_t windows = cdiv(T, 64), in = std::min<int64_t>(64, T), most = std::min(in, d->n_adapters + in / 16);
     auto slots = [&](int64_t blocks) { return static_cast<int>(std::max<int64_t>(1, std::min(most, blocks))); };
     p.slots_down = slots(2048 / (windows * p.parts));
     p.slots_up = slots(4096 / (windows * p.col_blocks));
@@ -232,6 +232,7 @@ int moe_proj_lora(const moe_proj_adapters* adapters, const uint16_t* x, int64_t 
   a.K = d->in_features;
   a.N = d->out_features;
   a.vr = static_cast<int32_t>(cdiv(d->max_rank, 16) * 16);
+  a.bits = 64 - __builtin_clzll(static_cast<unsigned long long>(d->n_adapters));
   a.parts = static_cast<int32_t>(p.parts);
   a.part_chunks = static_cast<int32_t>(p.part_chunks);
   hipStream_t s = static_cast<hipStream_t>(stream);
