@@ -270,7 +270,7 @@ AttnArgs attn_args(const moe_attn_config* c, const moe_attn_cache* cache, const 
 // How a decode call behind a shared prefix is cut: the prefix's tiles in parts for the columns of the whole batch,
 // and each sequence's own tiles in parts.
 struct SharedPlan {
-  bool wide;                         // the prefix in column blocks of k_attn_prefill, not of k_attn_decode
+  int wide;                          // wavefronts of k_attn_prefill's blocks, which take the prefix; 0: k_attn_decode's do
   int p_splits, p_tiles_per_split, splits, tiles_per_split;
   int col_blocks;                    // wide: of the prefix
   bool again;                        // several blocks read the same keys
@@ -281,47 +281,62 @@ struct SharedPlan {
   size_t ws_bytes;
 };
 
-constexpr int64_t SHARED_WIDE = 64;  // columns of a key/value head from which the prefix is taken in wide blocks
+template <int D, int NW>
+void plan_wide(SharedPlan& p, int64_t p_cols, int64_t kv_heads, int64_t shared) {
+  using S = PrefillShape<D, NW>;
+  const int64_t col_blocks = cdiv(p_cols, S::COLS), busy = col_blocks * kv_heads, tiles = cdiv(shared, S::TS);
+  const int64_t size = std::max(cdiv(busy * tiles, 256 * S::PER_CU), PF_LEAST);
+  p.wide = NW;
+  p.col_blocks = static_cast<int>(col_blocks);
+  p.p_tiles_per_split = static_cast<int>(size);
+  p.p_splits = static_cast<int>(cdiv(tiles, size));
+  p.p_blocks = busy * p.p_splits;
+}
 
 template <int D>
 SharedPlan shared_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len, int64_t shared) {
-  constexpr int NW = 4;
-  using S = PrefillShape<D, NW>;
   SharedPlan p{};
   const int64_t group = c->n_heads / c->n_kv_heads, cols = n_q * group, p_cols = B * cols, rows = p_cols * c->n_kv_heads;
   int64_t tiles = cdiv(max_len, 32) - shared / 32;
   if (c->window)
     tiles = std::min(tiles, cdiv(int64_t(c->window) + n_q, 32) + 1 + cdiv(std::max<int64_t>(c->n_sinks - shared, 0), 32) + 1);
-  const int64_t p_tiles = cdiv(shared, 32);
-  const int64_t col_blocks = cdiv(cols, 32), p_col_blocks = cdiv(p_cols, 32);
-  const int64_t places = 256 * attn_blocks_per_cu(D);
-  auto round = [](int64_t tps) {
-    tps = cdiv(tps, ATTN_NW) * ATTN_NW;
-    return tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
-  };
-  p.wide = p_cols > SHARED_WIDE;
-  const int64_t own = B * c->n_kv_heads * col_blocks * tiles, lead = p.wide ? 0 : c->n_kv_heads * p_col_blocks * p_tiles;
-  const int64_t tps = round(cdiv(own + lead, places));
+  const int64_t p_tiles = cdiv(shared, 32), col_blocks = cdiv(cols, 32), p_col_blocks = cdiv(p_cols, 32);
+  const int64_t lead = c->n_kv_heads * p_col_blocks * p_tiles;      // the prefix in k_attn_decode's blocks
+  // There, every 32 columns read the prefix again, out of an L2, in the same launch as the own keys: FEW_PS a tile of
+  // all blocks.  k_attn_prefill's blocks read it once for 128 or 256 columns, in a launch of their own, about 14 us
+  // with nothing to do, TILE_NS * 1.6 a tile of a block, and parts of more columns to join.  32/8 heads of 128 dims:
+  // 32 sequences behind 16384 keys 37 us, and 48 us wide; 64 behind 4096 32 and 38 us; 64 behind 32768 89 us wide
+  // (and over 120 us); 24 of 4 tokens of 24/8 heads of 64 dims behind 7919 29 and 37 us; 128 of 16/1 heads of 256 dims
+  // behind 2048 36 us wide, and 53 us.
+  constexpr int64_t FEW_PS = D == 64 ? 500 : D == 128 ? 1250 : 8000;
+  constexpr int64_t TILE_NS = D == 64 ? 600 : D == 256 ? 780 : 550;
+  SharedPlan w{};
+  plan_wide<D, 4>(w, p_cols, c->n_kv_heads, shared);
+  if (lead * FEW_PS / 1000 > 14000 + w.p_tiles_per_split * TILE_NS * 8 / 5 + rows * w.p_splits * D * 8 / 6000) {
+    p = w;
+    // as with prompts: long blocks that fill the GPU share their transfers among 8 wavefronts
+    if constexpr (D == 128) {
+      if (p_tiles > 64 && w.col_blocks * c->n_kv_heads * p_tiles > 16 * 512)
+        plan_wide<D, 8>(p, p_cols, c->n_kv_heads, shared);
+    }
+  }
+  // parts as in decode_plan, of the prefix too where the same launch takes it
+  const int64_t places = 256 * attn_blocks_per_cu(D), own = B * c->n_kv_heads * col_blocks * tiles;
+  int64_t tps = cdiv(cdiv(own + (p.wide ? 0 : lead), places), ATTN_NW) * ATTN_NW;
+  tps = tps < ATTN_NW ? ATTN_NW : tps > ATTN_MAX_TPS ? ATTN_MAX_TPS : tps;
   p.tiles_per_split = static_cast<int>(tps);
   p.splits = tiles > 0 ? static_cast<int>(cdiv(tiles, tps)) : 1;
   p.blocks = B * c->n_kv_heads * p.splits;
   if (col_blocks > 1) p.blocks = cdiv(p.blocks, 8) * 8 * col_blocks;
   p.again = col_blocks > 1 || (!p.wide && p_col_blocks > 1);
-  if (p.wide) {
-    const int64_t wide_tiles = cdiv(shared, S::TS), busy = cdiv(p_cols, S::COLS) * c->n_kv_heads;
-    p.col_blocks = static_cast<int>(cdiv(p_cols, S::COLS));
-    const int64_t size = std::max(cdiv(busy * wide_tiles, 256 * S::PER_CU), PF_LEAST);
-    p.p_tiles_per_split = static_cast<int>(size);
-    p.p_splits = static_cast<int>(cdiv(wide_tiles, size));
-    p.p_blocks = busy * p.p_splits;
-  } else {
+  if (!p.wide) {
     p.p_tiles_per_split = static_cast<int>(tps);
     p.p_splits = static_cast<int>(cdiv(p_tiles, tps));
     p.p_blocks = c->n_kv_heads * p.p_splits;
     if (p_col_blocks > 1) p.p_blocks = cdiv(p.p_blocks, 8) * 8 * p_col_blocks;
     p.blocks += p.p_blocks;
   }
-  p.join_waves = rows < 1024 ? 4 : 1;            // as at k_attn_join
+  p.join_waves = rows < 1024 ? 4 : 1;            // measured at k_attn_shared_join
   p.join_blocks = cdiv(rows, 4 / p.join_waves);
   p.p_items = rows * p.p_splits;
   p.items = rows * p.splits;
@@ -337,9 +352,12 @@ int validate_shared(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t ma
 
 template <int D>
 int decode_shared(AttnArgs a, const SharedPlan& p, hipStream_t s) {
-  if (p.wide && p.p_splits) {
+  if (p.wide) {
     a.col_blocks = p.col_blocks;
-    const int st = launch(k_attn_prefill<D, 4, true>, dim3(static_cast<unsigned>(p.p_blocks)), dim3(256), s, a);
+    const dim3 grid(static_cast<unsigned>(p.p_blocks)), block(p.wide * 64);
+    int st;
+    if constexpr (D == 128) st = launch(p.wide == 8 ? k_attn_prefill<D, 8, true> : k_attn_prefill<D, 4, true>, grid, block, s, a);
+    else st = launch(k_attn_prefill<D, 4, true>, grid, block, s, a);
     if (st) return st;
   }
   const int st = launch(p.again ? k_attn_decode<D, true, true> : k_attn_decode<D, false, true>,
