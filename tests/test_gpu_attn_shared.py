@@ -46,7 +46,8 @@ class Shared:
                     at += 1
                     for t in own[seen[own]]:
                         AO.store(kc, vc, table[b, j], t % P, ok[t - shared], ov[t - shared])
-            self.rows.append((qd[b], np.concatenate([pk[:n], ok]), np.concatenate([pv[:n], ov])))
+            self.rows.append((qd[b], ok, ov))
+        self.lead = pk, pv
         for j in range(lead):
             hit = np.nonzero(seen_lead[j * P:(j + 1) * P])[0] + j * P
             if hit.size:
@@ -75,6 +76,7 @@ class Shared:
         cfg, D = self.cfg, self.cfg.head_dim
         got, want, bound = out.double().cpu().numpy(), np.zeros(tuple(out.shape)), np.zeros(tuple(out.shape))
         for b, (q, k, v) in enumerate(self.rows):
+            k, v = (np.concatenate([t[:self.lens[b]], own]) for t, own in zip(self.lead, (k, v)))
             o, mag, big = AO.attend(q, k, v, cfg.scale, cfg.window, cfg.n_sinks)
             want[b] = o
             bound[b] = U * (mag + np.abs(o)) + (2 * (D + 16) * E * big + 2.0 ** -14) * mag
@@ -95,7 +97,7 @@ def case(heads, kv, dim, page, shared, lens, n_q=1, window=0, sinks=0, seed=0, *
 @pytest.mark.parametrize("shared", [0, 1, 15, 16, 31, 32, 33, 100, 256, 777])
 def test_prefix_lengths(dim, shared):
     case(8, 2, dim, 16, shared, [shared + n for n in (1, 40, 7)], seed=shared)
-    case(8, 2, dim, 32, shared, [shared + n for n in (1, 64, 100, 33)] * 8, seed=shared + 1)     # wide blocks
+    case(8, 2, dim, 32, shared, [shared + n for n in (1, 64, 100, 33)] * 8, seed=shared + 1)
 
 
 @pytest.mark.parametrize("dim,page", [(64, 256), (128, 128), (256, 64)])
@@ -137,6 +139,66 @@ def test_windows(dim, window, sinks):
 def test_long_prefixes(dim, heads, kv):
     case(heads, kv, dim, 64, 4099, [4099 + n for n in (1, 900, 17)], seed=1, v_mean=0.5)
     case(heads, kv, dim, 64, 4099, [4099 + n for n in (1, 900, 17, 5, 300)] * 6, seed=2, v_mean=0.5)
+
+
+# Sizes whose prefix is taken in wide column blocks (tests below run the same masks in both forms): heads, key/value
+# heads, dims, page, prefix, sequences; with 128 dims in blocks of 4 wavefronts and of 8.
+WIDE = [(64, 8, 64, 32, 13001, 128), (32, 8, 128, 16, 16379, 64), (64, 4, 128, 64, 9001, 64), (16, 1, 256, 64, 4100, 64)]
+
+
+def check_on_gpu(s, out, what):
+    """Shared.check with the definition in fp64 on the GPU, all sequences of a key/value head at once."""
+    cfg, P, B, M = s.cfg, s.shared, len(s.lens), s.n_q
+    G, D, top = cfg.n_heads // cfg.n_kv_heads, cfg.head_dim, max(1, max(n - s.shared for n in s.lens))
+    q = torch.from_numpy(np.stack([r[0] for r in s.rows])).to(DEV)                      # [B, M, H, D]
+    at = torch.tensor(s.lens, device=DEV)[:, None] - M + torch.arange(M, device=DEV)     # [B, M]
+    want, bound = torch.zeros_like(q), torch.zeros_like(q)
+    for h in range(cfg.n_kv_heads):
+        kp, vp = (torch.from_numpy(np.ascontiguousarray(t[:, h])).to(DEV) for t in s.lead)
+        ko, vo = torch.zeros((2, B, top, D), dtype=torch.float64, device=DEV)
+        for b, (_, k, v) in enumerate(s.rows):
+            ko[b, :len(k)], vo[b, :len(k)] = torch.from_numpy(k[:, h]).to(DEV), torch.from_numpy(v[:, h]).to(DEV)
+        mine = q[:, :, h * G:(h + 1) * G]
+
+        def over(f):
+            return torch.cat([f(mine) @ f(kp).T, torch.matmul(f(mine), f(ko)[:, None].transpose(-1, -2).contiguous())],
+                             dim=-1) * cfg.scale
+        key = torch.arange(P + top, device=DEV)
+        see = key <= at[..., None]
+        if cfg.window:
+            see &= (at[..., None] - key < cfg.window) | (key < cfg.n_sinks)
+        see = see[:, :, None]
+        w = over(lambda t: t).masked_fill(~see, -torch.inf)
+        w = (w - w.amax(-1, keepdim=True).clamp(min=-1e300)).exp()
+        w /= w.sum(-1, keepdim=True).clamp(min=1e-300)
+        big = float(over(torch.abs).masked_fill(~see, 0.0).max())
+        o, mag = (w[..., :P] @ f(vp) + torch.matmul(w[..., P:], f(vo)[:, None].contiguous())
+                  for f in (lambda t: t, torch.abs))
+        want[:, :, h * G:(h + 1) * G] = o
+        bound[:, :, h * G:(h + 1) * G] = U * (mag + o.abs()) + (2 * (D + 16) * E * big + 2.0 ** -14) * mag
+    assert_within(out.double().cpu().numpy(), want.cpu().numpy(), bound.cpu().numpy(), what)
+
+
+@pytest.mark.parametrize("heads,kv,dim,page,shared,B", WIDE)
+@pytest.mark.parametrize("kind", ["behind", "window", "inside", "verify"])
+def test_wide_blocks(heads, kv, dim, page, shared, B, kind):
+    """All columns see the whole prefix; a window that ends in it, with sinks; sequences that end inside it, or have
+    nothing; several new tokens, some without a position."""
+    window, sinks, n_q = 0, 0, 1
+    if kind == "behind":
+        lens = [shared + 1 + 29 * (b % 5) for b in range(B)]
+    elif kind == "window":
+        window, sinks = 700, 37
+        lens = [shared + 1 + 211 * (b % 6) for b in range(B)]
+    elif kind == "inside":
+        lens = [(0, 1, 31, 32, 129, shared - 1, shared, shared + 1)[b % 8] for b in range(B)]
+    else:
+        n_q, B = 4, B // 4
+        lens = [(2, 70, shared + 4, shared + 90)[b % 4] for b in range(B)]
+    what = f"wide: {heads}/{kv}x{dim}, {B} x {n_q} behind {shared}, {kind}"
+    print(f"[case] {what}", flush=True)
+    s = Shared(config(heads, kv, dim, page, window, sinks), shared, lens, n_q, seed=dim + B)
+    check_on_gpu(s, s.run(), what)
 
 
 @pytest.mark.parametrize("B", [3, 40])
