@@ -138,9 +138,8 @@ int moe_proj_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
       !stride_ok(x_stride, hidden))
     return MOE_MLP_ERR_BAD_SHAPE;
   if (!std::isfinite(eps) || eps < 0.0f) return MOE_MLP_ERR_BAD_VALUE;
-  if ((!y_out && !q_out) || !q_out != !q_scale) return MOE_MLP_ERR_NULL_ARG;
   if (T == 0) return MOE_MLP_OK;
-  if (!x) return MOE_MLP_ERR_NULL_ARG;
+  if (!x || (!y_out && !q_out) || !q_out != !q_scale) return MOE_MLP_ERR_NULL_ARG;
   if (!aligned(x) || !aligned(residual) || !aligned(weight) || !aligned(h_out) || !aligned(y_out) || !aligned(q_out) ||
       !aligned(q_scale))
     return MOE_MLP_ERR_MISALIGNED;
