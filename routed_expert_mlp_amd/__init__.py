@@ -6,8 +6,8 @@ attention.py that of the attention operators over a paged key/value cache, and
 projection.py that of what stands around the two: norms, FP8 projections, adapters.
 """
 from .attention import (AttnConfig, KVCache, moe_attn_decode, moe_attn_decode_shared, moe_attn_prefill,  # noqa: F401
-                        moe_attn_prepare, moe_attn_shared_workspace_size, moe_attn_workspace_bound,
-                        moe_attn_workspace_size, new_cache)
+                        moe_attn_prepare, moe_attn_shared_workspace_bound, moe_attn_shared_workspace_size,
+                        moe_attn_workspace_bound, moe_attn_workspace_size, new_cache)
 from .capi import (Config, KIND_DENSE, KIND_ROUTED, MoeMlpError, Weights, lib,  # noqa: F401
                    moe_mlp_decode, moe_mlp_prefill, moe_mlp_status_string, moe_mlp_workspace_size,
                    moe_nvfp4_dequant, moe_router_topk, workspace)

@@ -4,15 +4,15 @@ The attention half of the decoder layer whose MLP half capi.py binds: head
 norms, rotation and cache append of new tokens (moe_attn_prepare), attention of
 a few new tokens per sequence over the paged cache (moe_attn_decode), of a batch
 that shares a prefix (moe_attn_decode_shared), and of prompts or pieces of prompts
-(moe_attn_prefill).  As in capi.py, every function
-checks dtype, shape, device and contiguity of its tensors, passes their device
-pointers and torch's current HIP stream, and raises MoeMlpError on a non-zero
-status; the library does all of the computing.
+(moe_attn_prefill).  As in capi.py, every function checks dtype, shape, device and
+contiguity of its tensors, passes their device pointers and torch's current HIP
+stream, and raises MoeMlpError on a non-zero status; the library does all of the
+computing.
 
-bind_prepare, bind_decode, bind_decode_shared and bind_prefill check and marshal once and return a
-callable that issues the call again on the same buffers (serving loops).  It
-goes to the stream given when binding; with none given, to torch's current
-stream of the buffers' device at the time of each call, so that it can be
+bind_prepare, bind_decode, bind_decode_shared and bind_prefill check and marshal
+once and return a callable that issues the call again on the same buffers (serving
+loops).  It goes to the stream given when binding; with none given, to torch's
+current stream of the buffers' device at the time of each call, so that it can be
 called, or captured, under another stream than it was bound under.  Calls of one
 callable share its workspace: two of them must not run at the same time, and a
 graph that has captured one needs the callable for as long as it is replayed.
@@ -34,7 +34,8 @@ MAX_HEADS = 1024
 DECODE_MAX_Q = 8
 
 EXPORTED = ("moe_attn_prepare", "moe_attn_workspace_size", "moe_attn_workspace_bound", "moe_attn_decode",
-            "moe_attn_prefill", "moe_attn_decode_shared", "moe_attn_shared_workspace_size")
+            "moe_attn_prefill", "moe_attn_decode_shared", "moe_attn_shared_workspace_size",
+            "moe_attn_shared_workspace_bound")
 
 
 class moe_attn_config(ctypes.Structure):
@@ -63,6 +64,7 @@ def _lib() -> ctypes.CDLL:
         L.moe_attn_decode.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         L.moe_attn_decode_shared.argtypes = [cfgp, cp, vp, i64, i64, vp, vp, i64, i64, vp, i64, vp, vp, sz, vp]
         L.moe_attn_shared_workspace_size.argtypes = [cfgp, i64, i64, i64, i64, ctypes.POINTER(sz)]
+        L.moe_attn_shared_workspace_bound.argtypes = [cfgp, i64, i64, i64, ctypes.POINTER(sz)]
         L.moe_attn_prefill.argtypes = [cfgp, cp, vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, sz, vp]
         for n in EXPORTED:
             getattr(L, n).restype = ctypes.c_int
@@ -144,10 +146,18 @@ def workspace(cfg: AttnConfig, T: int, B: int, max_q: int, max_len: int, prefill
 
 def moe_attn_shared_workspace_size(cfg: AttnConfig, B: int, n_q: int, max_len: int, shared_len: int) -> int:
     """Bytes of moe_attn_decode_shared for n_q new tokens of B sequences of at most max_len tokens, the first shared_len
-    of which they share."""
+    of which they share; of exactly these sizes, since smaller ones may need more (moe_attn_shared_workspace_bound)."""
+    return _shared_size("moe_attn_shared_workspace_size", cfg, B, n_q, max_len, shared_len)
+
+
+def moe_attn_shared_workspace_bound(cfg: AttnConfig, B: int, n_q: int, max_len: int) -> int:
+    """Bytes for every call of moe_attn_decode_shared of these sizes or smaller ones, whatever is shared."""
+    return _shared_size("moe_attn_shared_workspace_bound", cfg, B, n_q, max_len)
+
+
+def _shared_size(name, cfg, *sizes) -> int:
     n = ctypes.c_size_t(0)
-    _check(_lib().moe_attn_shared_workspace_size(ctypes.byref(cfg.c()), int(B), int(n_q), int(max_len), int(shared_len),
-                                                 ctypes.byref(n)), "moe_attn_shared_workspace_size")
+    _check(getattr(_lib(), name)(ctypes.byref(cfg.c()), *map(int, sizes), ctypes.byref(n)), name)
     return n.value
 
 

@@ -344,6 +344,17 @@ SharedPlan shared_plan(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t
   return p;
 }
 
+// The most workspace of such a call with no larger sizes.  Items are rows x parts, of the own keys and of the prefix.
+// Parts shorter than ATTN_MAX_TPS tiles are at most as many as there are places, and one for each block, of 32 columns
+// in k_attn_decode and of 128 or 256 in k_attn_prefill (places x columns: 2^16 at most); the others are as many as the
+// longest sequence has.
+size_t shared_bound(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len) {
+  const int64_t rows = B * n_q * c->n_heads, tiles = cdiv(max_len, 32);
+  const int64_t items = std::min(rows * std::max<int64_t>(cdiv(tiles, ATTN_NW), 1),
+                                 std::max((int64_t(1) << 16) + rows, rows * cdiv(tiles, ATTN_MAX_TPS)));
+  return size_t(2 * items) * (c->head_dim + 2) * 4;
+}
+
 int validate_shared(const moe_attn_config* c, int64_t B, int64_t n_q, int64_t max_len, int64_t shared) {
   const int st = validate_sizes(c, 0, B, n_q, max_len, 0);
   if (st) return st;
@@ -531,6 +542,16 @@ int moe_attn_shared_workspace_size(const moe_attn_config* cfg, int64_t B, int64_
     *bytes = p.ws_bytes;
     return MOE_MLP_OK;
   });
+}
+
+int moe_attn_shared_workspace_bound(const moe_attn_config* cfg, int64_t B, int64_t n_q, int64_t max_len,
+                                    size_t* bytes) {
+  size_t need = 0;
+  const int st = moe_attn_shared_workspace_size(cfg, B, n_q, max_len, 0, &need);
+  if (st) return st;
+  if (!bytes) return MOE_MLP_ERR_NULL_ARG;
+  *bytes = B ? shared_bound(cfg, B, n_q, max_len) : 0;
+  return MOE_MLP_OK;
 }
 
 int moe_attn_decode_shared(const moe_attn_config* cfg, const moe_attn_cache* cache, const uint16_t* q, int64_t B,

@@ -2,6 +2,7 @@
 fake device addresses are safe)."""
 import ctypes
 import math
+import random
 
 import pytest
 
@@ -72,3 +73,42 @@ def test_sizes_of_many_calls(dim, heads, kv):
                         assert st == 0 and need > 0
                         assert call(c, cache(), B=B, n_q=n_q, max_pages=1 << 20, max_len=shared + own, shared=shared,
                                     wsb=need - 1) == capi.ERR_WORKSPACE_TOO_SMALL
+
+
+def bound(c, B, n_q, max_len):
+    n = ctypes.c_size_t(0)
+    st = A._lib().moe_attn_shared_workspace_bound(ctypes.byref(c) if c is not None else None, B, n_q, max_len,
+                                                  ctypes.byref(n))
+    return st, n.value
+
+
+def test_bound_refusals():
+    assert bound(None, 2, 1, 64)[0] == capi.ERR_NULL_ARG
+    assert bound(cfg(head_dim=96), 2, 1, 64)[0] == capi.ERR_BAD_SHAPE
+    assert bound(cfg(), 2, 0, 64)[0] == capi.ERR_BAD_SHAPE
+    assert bound(cfg(), -1, 1, 64)[0] == capi.ERR_BAD_SHAPE
+    assert bound(cfg(), 0, 1, 64) == (0, 0)
+    assert A._lib().moe_attn_shared_workspace_bound(ctypes.byref(cfg()), 2, 1, 64, None) == capi.ERR_NULL_ARG
+
+
+def _spread(rng, high):
+    """A size up to high, over its logarithm, the ends among them."""
+    return rng.choice([high, max(1, int(round(math.exp(rng.uniform(0, math.log(high + 1)))))), rng.randint(1, high)])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_bound_is_enough_for_smaller_calls(seed):
+    rng = random.Random(seed)
+    for _ in range(150):
+        kv = rng.choice([1, 2, 3, 8])
+        window = rng.choice([0, 0, 500, 1 << 20])
+        c = cfg(head_dim=rng.choice([64, 128, 256]), n_kv_heads=kv, n_heads=kv * rng.choice([1, 3, 4, 16, 64]),
+                window=window, n_sinks=rng.choice([0, 4, 3000]))
+        B, n_q, max_len = _spread(rng, 512), rng.randint(1, 8), _spread(rng, 300000)
+        st, most = bound(c, B, n_q, max_len)
+        assert st == 0
+        for _ in range(12):
+            b, n, m = _spread(rng, B), rng.randint(1, n_q), _spread(rng, max_len)
+            for shared in (0, m, m // 2, max(0, m - 100), rng.randint(0, m)):
+                st, need = size(c, min(b, B), n, min(m, max_len), min(shared, m, max_len))
+                assert st == 0 and need <= most, (B, n_q, max_len, b, n, m, shared)
