@@ -66,6 +66,17 @@ def test_norm_small_and_large_rows():
     norm_case(9, 640, True, True, "hyq", 7, std=2.0 ** -40)
 
 
+def test_norm_ends_of_the_range():
+    """Squares whose sum is close to the largest fp32 in the widest row, and the least sum that eps 0 allows."""
+    for H, value in ((16384, 2.0 ** 56), (16384, -2.0 ** 56), (128, 2.0 ** -53), (16384, 2.0 ** -56)):
+        x = torch.full((2, H), value, dtype=torch.bfloat16)
+        x[1, ::3] *= -0.5
+        y, q = torch.empty((2, H), dtype=torch.bfloat16, device=DEV), torch.empty((2, H), dtype=torch.uint8, device=DEV)
+        s = torch.empty((2, H // 128), dtype=torch.float32, device=DEV)
+        P.moe_proj_norm(x.to(DEV), None, 0.0, None, None, y, q, s)
+        check_norm(x.double().numpy(), None, None, 0.0, None, y, q, s, f"norm of {H} of {value}")
+
+
 def test_norm_rows_of_zeros_and_not_finite():
     T, H = 8, 392
     x = torch.randn((T, H), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
@@ -135,9 +146,15 @@ def test_fp8_sums(K):
     fp8_case(160, 144, K, K)
 
 
-def test_fp8_larger_calls():
-    fp8_case(1100, 1040, 512, 1)
-    fp8_case(2049, 528, 256, 2)
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 896, 1152])
+def test_fp8_larger_calls(K):
+    """Tiles of 128 x 128 and of 256 x 256, with rows past their ends, and with a number of spans that leaves a group
+    of scales unfilled at the end of the last row."""
+    fp8_case(1100, 1040, K, 1)
+    fp8_case(1024, 1024, K, 2)
+    fp8_case(2049, 528, K, 3)
+    fp8_case(3000, 2960, K, 4)
+    fp8_case(2305, 3600, K, 5)
 
 
 def test_fp8_keeps_not_finite_rows_to_themselves():
@@ -222,6 +239,19 @@ def test_lora_features(K, N):
 def test_lora_strides(in_place):
     lora_case(70, 128, 264, 32, 5, mixed(70, 5, 1), 1, in_place=in_place, pad=(8, 40, 24), what="columns of wider tensors")
     lora_case(70, 128, 264, 32, 5, mixed(70, 5, 2), 2, scales=False, in_place=in_place)
+
+
+@pytest.mark.parametrize("n", [511, 512, 700])
+@pytest.mark.parametrize("T", [1, 64, 65, 200, 330])
+def test_lora_many_adapters(T, n):
+    """More adapters than one block sorts by: windows of 64 tokens; and the most that it does."""
+    lora_case(T, 72, 136, 8, n, mixed(T, n, T + n), T + n, ranks=[1 + i % 8 for i in range(n)], what="many adapters")
+
+
+def test_lora_sorts_long_calls():
+    """More tokens than a wavefront of the sorting block holds at once, in any order and in runs."""
+    lora_case(9000, 64, 72, 8, 5, mixed(9000, 5, 3), 3, what="any order")
+    lora_case(8193, 64, 72, 8, 300, np.sort(mixed(8193, 300, 4))[::-1].copy(), 4, what="falling")
 
 
 def test_lora_runs_and_extremes():
