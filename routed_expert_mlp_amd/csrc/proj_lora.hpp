@@ -440,7 +440,7 @@ __device__ __forceinline__ void lora_columns(const LoraArgs& a, const Tile& tile
 // Rows of the output: .y = 256 columns, 64 a wavefront.
 template <bool GROUPED>
 __global__ __launch_bounds__(64 * LORA_UP, GROUPED ? 3 : 4) void k_lora_up(LoraArgs a) {
-  extern __shared__ uint4 vl[];                  // [64 tokens][2 halves][pitch] pieces of 8 values
+  extern __shared__ uint4 vl[];                  // [tokens of a tile: 64 grouped, else 16][2 halves][pitch] pieces of 8 values
   const int n0 = blockIdx.y * (64 * LORA_UP) + 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   lora_tiles<GROUPED>(a, [&](const auto& tile) __attribute__((always_inline)) {
     if (tile.adapter < 0) {                      // base as it is, 8 tokens at a time

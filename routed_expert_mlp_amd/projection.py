@@ -26,8 +26,8 @@ from typing import Optional
 import torch
 
 from . import attention, capi
-from .attention import _one_device
-from .capi import _check, _check_tensor, _ptr, _stream
+from .attention import _bytes_on_stream, _one_device
+from .capi import _check, _check_tensor, _ptr
 
 BLOCK = capi.FP8_BLOCK
 NORM_MAX_HIDDEN = 16384
@@ -175,12 +175,7 @@ def bind_lora(adapters: Adapters, x: torch.Tensor, adapter: torch.Tensor, base: 
     xs, bs, os = (_rows(t, n, w, T) for n, t, w in (("x", x, K), ("base", base, N), ("out", out, N)))
     own = ws is None
     if own:
-        handle = _stream(stream)
-        if handle == torch.cuda.current_stream().cuda_stream:
-            ws = lora_workspace(adapters, T, x.device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
-                ws = lora_workspace(adapters, T, x.device)
+        ws = _bytes_on_stream(moe_proj_lora_workspace_size(adapters, T), x.device, stream)
     _check_tensor(ws, "workspace", None, torch.uint8)
     _one_device(a=adapters.a, b=adapters.b, ranks=adapters.ranks, scales=adapters.scales, x=x, adapter=adapter,
                 base=base, out=out, workspace=ws)
