@@ -58,21 +58,25 @@ int fp8_tile(const Fp8Args& a, hipStream_t s) {
   return launch(k_proj_fp8_tile<WN, WT, 4, TT>, grid, dim3(64 * WN * WT), s, a);
 }
 
-// The smallest blocks that the 256 CUs take at once, one each, since the reads of a
-// block do not get shorter when it is one of more (4096 columns; blocks of 16 x 16,
-// 32 x 16, 32 x 64, 64 x 64 outputs x tokens without LDS, 128 x 128 tiles):
-//   1 token to 4096: 6.0, 6.8 us; to 6144: 8.3, 7.1 us;
-//   32 to 1024: 6.2, 8.8, 11.6 us; 48 to 6144: -, -, 13.8, 18.4, 23.4 us;
-//   128 to 6144: -, -, 28.1, 20.3, 24.5 us; 700 to 1536: -, -, 39, 38, 24.5 us.
-// Past that, tiles of 128 x 128 while their blocks, two a CU, have places at once, and
-// of 256 x 256 then (2048 to 4096: 39 and 52 us; 1536 to 6144: 58 and 53 us).  Up to 16
-// tokens the weights' stream is all there is, however long.
+// The smallest blocks that the 256 CUs take at once, one each: a block's time is that of
+// its chain of reads (4096 columns; blocks of 16 x 16, 32 x 16, 32 x 32, 64 x 32, 64 x 64
+// outputs x tokens, tiles of 128 x 128; us, those not shown are slower):
+//   1 token to 1024: 3.8, 4.5; 64 to 2048: 5.9, 5.7, 6.5; 32 to 6144: 9.5, 9.3, 8.4, 9.3;
+//   64 to 6144: -, 12.3, 11.1, 9.9, 12.9; 128 to 6144: -, 19.4, 15.5, 16.3, 13.1, 24.7.
+// Up to 16 tokens the weights' stream is all there is, and small blocks may share a CU
+// (to 6144: 7.1, 7.4; to 12288: 10.7, 11.9; 2048 to 16384: 10.0, 7.8).  Past one block of
+// 64 x 64 a CU, up to five of 32 x 32 (700 to 1536: -, -, 19.1, 21.9, 22.7, 24.8; 300 to
+// 4096: -, -, 20.8, 22.5, 23.0, 24.2; 384 to 6144, nine of them: -, -, 34.6, 36.5, 33.8,
+// 25.3), then tiles of 128 x 128 while their blocks, two a CU, have places at once, and
+// of 256 x 256 after that (2048 to 4096: 39 and 52 us; 1536 to 6144: 58 and 53 us).
 int fp8(const Fp8Args& a, hipStream_t s) {
   auto blocks = [&](int n, int t) { return cdiv(a.N, n) * cdiv(a.T, t); };
-  if (blocks(16, 16) <= 256) return fp8_few<1, 1, 4>(a, s);
+  if (blocks(16, 16) <= (a.T <= 16 ? 768 : 256)) return fp8_few<1, 1, 4>(a, s);
   if (a.T <= 16 || blocks(32, 16) <= 256) return fp8_few<2, 1, 2>(a, s);
-  if (blocks(32, 64) <= 256) return fp8_few<2, 4, 2>(a, s);
+  if (blocks(32, 32) <= 256) return fp8_few<2, 2, 2>(a, s);
+  if (blocks(64, 32) <= 256) return fp8_few<4, 2, 1>(a, s);
   if (blocks(64, 64) <= 256) return fp8_few<4, 4, 1>(a, s);
+  if (blocks(32, 32) <= 5 * 256) return fp8_few<2, 2, 2>(a, s);
   if (blocks(128, 128) <= 512) return fp8_tile<2, 2, 4>(a, s);
   return fp8_tile<4, 2, 8>(a, s);
 }

@@ -47,13 +47,17 @@ __device__ __forceinline__ i32x8 operand(const uint4* p, const uint4* q) {
 }
 
 // Few tokens, or few outputs: a block takes 16 NT rows of the weights and 16 MT
-// tokens, its NW wavefronts every NW'th span, straight from memory into the operand
-// registers, U spans at a time in flight; they join in LDS, pair by pair.
+// tokens, its NW wavefronts every NW'th span; they join in LDS, pair by pair.
+// Eight lanes read a row's 128 bytes, whole lines, into registers, U spans at a time
+// in flight.  An operand has 16 rows in neighbouring lanes, so the lines go through
+// LDS of the wavefront's own, with no barrier; piece p of row r is at p ^ (r & 7), as
+// in the tiles below.  (Loads straight into operands touch 16 rows with each
+// instruction, and the addresses take the time: 517 tokens of 4096 columns to 576 15.3
+// us and 9.8 this way, 128 to 6144 20.2 and 13.1, 32 to 1024 6.2 and 3.9.)
 // What bounds it: the weights' stream with a token (4096 columns to 6144: 7 us, 3.6
-// TB/s with the launch in it), with more the reads of the tokens' rows, which every
-// block takes from L2 again: 48 tokens 14 us, 517 tokens to 576 columns 15.5 us.
-// The scales of four spans come in one load: a load of 16 rows' scales takes as long
-// as one of 16 bytes of each (517 tokens: 17.6 us with a load a span).
+// TB/s with the launch in it); with more, a block's reads from L2, their way through
+// LDS and the rounds of their latency.
+// The scales of four spans come in one load.
 template <int NT, int MT, int NW, int U>
 __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
@@ -61,17 +65,24 @@ __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
   const int rows = (a.N + 16 * NT - 1) / (16 * NT), n0 = static_cast<int>(blockIdx.x % rows) * (16 * NT), spans = a.K >> 7;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / rows) * (16 * MT);
   const float* const ws = a.ws + static_cast<int64_t>(n0 >> 7) * spans;
-  const uint8_t* wp[NT];
-  const uint8_t* xp[MT];
+  // loads: 8 rows of 128 bytes each; rows past the last one have the last one's again
+  constexpr int W = 2 * NT, L = 2 * (NT + MT);
+  __shared__ uint4 lines[NW][L * 64];
+  const int lr = lane >> 3, lp = lane & 7;
+  const uint8_t* const wbase = a.w + static_cast<int64_t>(n0) * a.K;
+  const uint8_t* const xbase = a.x + t0 * a.K;
+  const int last_n = a.N - 1 - n0, last_t = static_cast<int>(a.T - 1 - t0 < 16 * MT ? a.T - 1 - t0 : 16 * MT);
+  uint32_t off[L];
   const float* xs[MT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) wp[n] = a.w + static_cast<int64_t>(min(n0 + 16 * n + c, a.N - 1)) * a.K + 16 * g;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t t = min(t0 + 16 * m + c, a.T - 1);
-    xp[m] = a.x + t * a.K + 16 * g;
-    xs[m] = a.xs + t * spans;
+  for (int i = 0; i < L; ++i) {
+    const int row = i < W ? min(8 * i + lr, last_n) : min(8 * (i - W) + lr, last_t);
+    off[i] = static_cast<uint32_t>(row) * a.K + 16 * lp;
   }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) xs[m] = a.xs + (t0 + min(16 * m + c, last_t)) * spans;
+  uint4* const mine = lines[w];
+  const int put = 8 * lr + (lp ^ lr), p0 = 8 * c + (g ^ (c & 7)), p1 = 8 * c + ((g + 4) ^ (c & 7));
   f32x4 acc[NT][MT];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -86,39 +97,45 @@ __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
 #pragma unroll
     for (int u0 = 0; u0 < 4; u0 += U) {
       if (u0 && s4 + NW * u0 >= spans) continue;
-      i32x8 wf[U][NT], xf[U][MT];
+      i32x4 raw[U][L];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int s = min(s4 + NW * (u0 + u), spans - 1);    // past the end the last span, with scales of 0
+        const int64_t at = 128 * min(s4 + NW * (u0 + u), spans - 1);     // past the end the last span, with scales of 0
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4* const r = reinterpret_cast<const uint4*>(wp[n] + 128 * s);
-          wf[u][n] = operand(r, r + 4);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4* const r = reinterpret_cast<const uint4*>(xp[m] + 128 * s);
-          xf[u][m] = operand(r, r + 4);
-        }
+        for (int i = 0; i < L; ++i)
+          raw[u][i] = *reinterpret_cast<const i32x4*>((i < W ? wbase : xbase) + at + off[i]);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        // a wavefront's LDS operations are done in order
+#pragma unroll
+        for (int i = 0; i < L; ++i) *reinterpret_cast<i32x4*>(mine + 64 * i + put) = raw[u][i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        i32x8 wf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) wf[n] = operand(mine + 128 * n + p0, mine + 128 * n + p1);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+          const i32x8 xf = operand(mine + 128 * (NT + m) + p0, mine + 128 * (NT + m) + p1);
           const float f = __shfl(sc[m], 16 * (u0 + u) + c);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const f32x4 p = mfma_e4m3(wf[u][n], xf[u][m], f32x4{});
+            const f32x4 p = mfma_e4m3(wf[n], xf, f32x4{});
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[i], f, acc[n][m][i]);
           }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
     }
   }
-  __shared__ f32x4 part[NW / 2][NT][MT][64];
+  static_assert(sizeof(lines) >= sizeof(f32x4) * (NW / 2) * NT * MT * 64, "the sums fit where the lines were");
+  f32x4 (*const part)[NT][MT][64] = reinterpret_cast<f32x4 (*)[NT][MT][64]>(&lines[0][0]);
 #pragma unroll
   for (int step = NW / 2; step; step >>= 1) {
-    if (step < NW / 2) __syncthreads();
+    __syncthreads();
     if (w >= step && w < 2 * step) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)

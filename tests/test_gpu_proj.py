@@ -148,13 +148,12 @@ def test_fp8_sums(K):
 
 @pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 896, 1152])
 def test_fp8_larger_calls(K):
-    """Tiles of 128 x 128 and of 256 x 256, with rows past their ends, and with a number of spans that leaves a group
-    of scales unfilled at the end of the last row."""
-    fp8_case(1100, 1040, K, 1)
-    fp8_case(1024, 1024, K, 2)
-    fp8_case(2049, 528, K, 3)
-    fp8_case(3000, 2960, K, 4)
-    fp8_case(2305, 3600, K, 5)
+    """Blocks of every size (32 x 16, 32 x 32, 64 x 32, 64 x 64 and 32 x 32 again, tiles of 128 x 128, fewer and more
+    than the GPU has CUs, and of 256 x 256), with rows past their ends, and with numbers of spans that leave a group of
+    scales unfilled at the end of the last row."""
+    for i, (T, N) in enumerate(((100, 1040), (16, 12304), (200, 1040), (300, 1040), (700, 1040), (1024, 1024),
+                                (1100, 1040), (2049, 528), (1500, 1552), (2049, 2960), (3000, 2960), (2305, 3600))):
+        fp8_case(T, N, K, i)
 
 
 def test_fp8_keeps_not_finite_rows_to_themselves():
