@@ -253,7 +253,8 @@ int moe_proj_lora(const moe_proj_adapters* adapters, const uint16_t* x, int64_t 
   if (sd) return sd;
   a.slots = p.slots_up;
   return launch(p.grouped ? k_lora_up<true> : k_lora_up<false>,
-                dim3(static_cast<unsigned>(p.up_x), static_cast<unsigned>(p.col_blocks)), dim3(64 * LORA_UP), s, a,
+                dim3(static_cast<unsigned>(p.up_x), static_cast<unsigned>(p.col_blocks)),
+                dim3(64 * LORA_UP * (p.grouped ? 2 : 1)), s, a,
                 size_t(2 * (p.grouped ? 64 : 16)) * (a.vr / 8 + 1) * 16);
 }
 

@@ -6,14 +6,21 @@
 // time (a tile), in whatever order they come, so that an adapter is read once for
 // them.  Up to 64 tokens each block finds its adapter's tokens itself: every
 // wavefront reads the adapter numbers, one a lane, and lanes of one adapter find each
-// other with a ballot for each bit of its number.  With more, k_lora_group sorts the tokens by adapter first (4096
-// tokens of 50 adapters in any order: 466 us in windows of 64 tokens, each of which
-// reads most adapters again).
+// other with a ballot for each bit of its number.  With more, k_lora_group sorts the
+// tokens by adapter first (4096 tokens of 50 adapters in any order: 466 us in windows
+// of 64 tokens, each of which reads most adapters again, and 51 us sorted).
 //
 // v is a sum over thousands of columns, cut into parts for the blocks; k_lora_up
 // adds up the parts (fp32, in order), and gives v to the matrix unit as the sum of
 // two bf16 values, beside the bf16 weights: 16 bits of it, at the price of half a
 // matrix instruction more, where the time is that of the memory.
+//
+// What bounds it: with few tokens two launches, each with a chain of reads behind it
+// (adapter numbers, weights, parts); with many the rows, x once and base in and out
+// once, at two thirds of a copy's rate, and the sort.  4096 columns: one token of
+// rank 16 to 6144 10 us (5.0 and 5.6 in the kernels), 64 tokens of 32 adapters of
+// rank 64 to 6144 17 us (7.5 and 9.3: 3.2 TB/s), 4096 tokens of 5 adapters of rank 32
+// to 4096 38 us (sort 7.0, 12.2 for 34 MB and 19.5 for 67 MB).
 #pragma once
 
 #include "common.hpp"
@@ -21,6 +28,8 @@
 #include <type_traits>
 
 namespace moe {
+
+typedef int lora_piece __attribute__((ext_vector_type(4)));       // 16 bytes: 8 values
 
 struct LoraArgs {
   const uint16_t* a;
@@ -132,38 +141,45 @@ __global__ __launch_bounds__(64 * LORA_GROUP) void k_lora_group(LoraArgs a) {
   const int bins = static_cast<int>(a.n_adapters) + 1;
   const int run = static_cast<int>((a.T + 64 * LORA_GROUP - 1) / (64 * LORA_GROUP)) * 64;
   const int64_t t0 = static_cast<int64_t>(run) * w, t1 = t0 + run < a.T ? t0 + run : a.T;
-  for (int i = tid; i < LORA_GROUP * LORA_BINS; i += 64 * LORA_GROUP) count[i / LORA_BINS][i % LORA_BINS] = 0;
-  __syncthreads();
-  auto bin_of = [&](int64_t t) __attribute__((always_inline)) {
-    const int id = t < t1 ? a.adapter[t] : -1;
-    return id >= 0 && id < bins - 1 ? id : bins - 1;
-  };
-  auto alike = [&](int bin, bool in) __attribute__((always_inline)) {
-    uint64_t m = __ballot(in);
-    for (int b = 0; b < a.bits; ++b) {
-      const bool one = bin >> b & 1;
-      const uint64_t ones = __ballot(one);
-      m &= one ? ones : ~ones;
-    }
-    return m;
-  };
-  volatile int* const mine = count[w];
   constexpr int AHEAD = 8;                       // loads in flight
-  for (int64_t t8 = t0; t8 < t1; t8 += 64 * AHEAD) {
-    int next[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) next[i] = bin_of(t8 + 64 * i + lane);
+  int bin[AHEAD];
+  uint64_t same[AHEAD];                          // lanes of this lane's bin
+  auto read = [&](int64_t t8) __attribute__((always_inline)) {
+    int id[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const bool in = t8 + 64 * i + lane < t1;
-      const uint64_t m = alike(next[i], in);
-      if (in && __builtin_ctzll(m) == lane) mine[next[i]] = mine[next[i]] + __popcll(m);
+      const int64_t t = t8 + 64 * i + lane;
+      id[i] = t < t1 ? a.adapter[t] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      bin[i] = id[i] >= 0 && id[i] < bins - 1 ? id[i] : bins - 1;
+      same[i] = 0;
+      if (t8 + 64 * i >= t1) continue;
+      same[i] = __ballot(t8 + 64 * i + lane < t1);
+      for (int b = 0; b < a.bits; ++b) {
+        const bool one = bin[i] >> b & 1;
+        const uint64_t ones = __ballot(one);
+        same[i] &= one ? ones : ~ones;
+      }
+    }
+  };
+  read(t0);
+  const int rank = tid < bins - 1 ? lora_rank(a, tid) : 0;
+  volatile int* const mine = count[w];
+  for (int i = lane; i < bins; i += 64) mine[i] = 0;
+  for (int64_t t8 = t0; t8 < t1; t8 += 64 * AHEAD) {
+    if (t8 > t0) read(t8);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (t8 + 64 * i >= t1) continue;
+      if (t8 + 64 * i + lane < t1 && __builtin_ctzll(same[i]) == lane) mine[bin[i]] = mine[bin[i]] + __popcll(same[i]);
     }
   }
   __syncthreads();
   // of each bin: where the wavefronts' tokens go within it, its tokens and tiles in all
   int total = 0;
-  if (tid < LORA_BINS) {
+  if (tid < bins) {
     for (int i = 0; i < LORA_GROUP; ++i) {
       const int n = count[i][tid];
       count[i][tid] = total;
@@ -175,7 +191,7 @@ __global__ __launch_bounds__(64 * LORA_GROUP) void k_lora_group(LoraArgs a) {
   __syncthreads();
   int from = 0;
   for (int step = 1; step < bins; step <<= 1, from ^= 1) {
-    if (tid < LORA_BINS) {
+    if (tid < bins) {
       place[from ^ 1][tid] = place[from][tid] + (tid >= step ? place[from][tid - step] : 0);
       tile[from ^ 1][tid] = tile[from][tid] + (tid >= step ? tile[from][tid - step] : 0);
     }
@@ -183,110 +199,136 @@ __global__ __launch_bounds__(64 * LORA_GROUP) void k_lora_group(LoraArgs a) {
   }
   if (tid < bins) {
     const int first = place[from][tid] - total, tiles = (total + 63) >> 6;
-    const int rank = tid < bins - 1 ? lora_rank(a, tid) : 0;
+    for (int i = 0; i < LORA_GROUP; ++i) count[i][tid] += first;
     for (int i = 0; i < tiles; ++i)
       a.tiles[tile[from][tid] - tiles + i] =
           int4{tid == bins - 1 ? -1 : tid, first + 64 * i, min(total - 64 * i, 64), rank};
-    for (int i = 0; i < LORA_GROUP; ++i) count[i][tid] += first;
     if (tid == bins - 1) *a.n_tiles = tile[from][tid];
   }
   __syncthreads();
   for (int64_t t8 = t0; t8 < t1; t8 += 64 * AHEAD) {
-    int next[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) next[i] = bin_of(t8 + 64 * i + lane);
+    if (run > 64 * AHEAD) read(t8);              // otherwise they are here still
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const bool in = t8 + 64 * i + lane < t1;
-      const uint64_t m = alike(next[i], in);
-      if (in) {
-        const int at = mine[next[i]];
-        a.order[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = static_cast<int32_t>(t8 + 64 * i + lane);
-        if (__builtin_ctzll(m) == lane) mine[next[i]] = at + __popcll(m);
-      }
+      if (t8 + 64 * i + lane >= t1) continue;
+      const int at = mine[bin[i]];
+      a.order[at + __popcll(same[i] & ((uint64_t(1) << lane) - 1))] = static_cast<int32_t>(t8 + 64 * i + lane);
+      if (__builtin_ctzll(same[i]) == lane) mine[bin[i]] = at + __popcll(same[i]);
     }
   }
 }
 
-// Sums of a wavefront over its chunks: MT tiles of 16 gathered tokens, RT tiles of 16 ranks.  Lanes of rows or ranks
-// past the last one have the last one's again; nobody reads what comes of it.
-template <int MT, int RT, typename Tile>
+// Writes of a wavefront to LDS, and its reads behind them: done in order, if the compiler keeps it.
+__device__ __forceinline__ void lora_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sums of a wavefront over its chunks of 64 columns: MT tiles of 16 gathered tokens, RT tiles of 16 ranks.  Eight lanes
+// read the 128 bytes of a row, which become operands (16 rows in neighbouring lanes) in LDS of the wavefront's own;
+// piece p of row r is at p ^ (r & 7), so that the rows of an operand fall to different banks.  Lanes of rows or ranks
+// past the last one have the last one's again; nobody reads what comes of it.  (LINES false: loads straight into
+// operands, with 16 rows an instruction: 64 tokens of 64 adapters of rank 16 6.2 and 8.7 us, where LDS is one more wait;
+// 32 adapters of rank 64 9.3 and 7.6 us, 4096 tokens 13.9 and 12.1 us.)
+template <int MT, int RT, bool LINES, typename Tile>
 __device__ __forceinline__ void lora_rows(const LoraArgs& a, const Tile& tile, int rank, int r0, int c0, int c1,
-                                          f32x4 (*acc)[LORA_RT]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+                                          f32x4 (*acc)[LORA_RT], uint4* mine) {
+  constexpr int X = 2 * MT, L = 2 * (MT + RT);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, lr = lane >> 3, lp = lane & 7;
   const int pieces = a.K >> 3;                   // of 8 columns
-  const uint4* xp[MT];
-  const uint4* ap[RT];
+  // row and piece of load i
+  auto row_of = [&](int i) __attribute__((always_inline)) { return LINES ? 8 * i + lr : 16 * (i >> 1) + c; };
+  auto piece_of = [&](int i) __attribute__((always_inline)) { return LINES ? lp : 4 * (i & 1) + g; };
+  const uint16_t* row[X];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xp[m] = reinterpret_cast<const uint4*>(a.x + tile.token(a, 16 * m + c) * a.x_stride) + g;
+  for (int i = 0; i < X; ++i) row[i] = a.x + tile.token(a, row_of(i)) * a.x_stride;
+  const uint16_t* const at = a.a + static_cast<int64_t>(tile.adapter) * a.R * a.K;
+  uint32_t off[L - X];                           // of rows of the adapter: at most 256 of less than 2^20 columns
 #pragma unroll
-  for (int n = 0; n < RT; ++n)
-    ap[n] = reinterpret_cast<const uint4*>(
-                a.a + (static_cast<int64_t>(tile.adapter) * a.R + min(r0 + 16 * n + c, rank - 1)) * a.K) + g;
+  for (int i = 0; i < L - X; ++i) off[i] = static_cast<uint32_t>(min(r0 + row_of(i), rank - 1)) * a.K;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < RT; ++n) acc[m][n] = f32x4{};
-  // a chunk is 64 columns: pieces g and 4 + g of 8
-  auto chunk = [&](int k, auto whole) __attribute__((always_inline)) {
-    bf16x8 xf[2][MT], af[2][RT];
+  lora_piece raw[L];
+  auto read = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      int p = 8 * k + 4 * h;
-      const bool in = decltype(whole)::value || p + g < pieces;
-      if (!in) p = -g;
+    for (int i = 0; i < L; ++i) {
+      const int p = 8 * k + piece_of(i);
+      const bool in = p < pieces;
+      const uint32_t k8 = 8 * (in ? p : 0);
+      raw[i] = *reinterpret_cast<const lora_piece*>(i < X ? row[i] + k8 : at + (off[i - X] + k8));
+      if (!in) raw[i] = lora_piece{};
+    }
+  };
+  const int put = 8 * lr + (lp ^ lr);
+  int k = c0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (k < c1) read(k);
+  for (; k < c1; k += LORA_DOWN) {
+    if constexpr (!LINES) {
 #pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        uint4 v = ap[n][p];
-        if (!in) v = uint4{};
-        af[h][n] = __builtin_bit_cast(bf16x8, v);
-      }
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint4 v = xp[m][p];
-        if (!in) v = uint4{};
-        xf[h][m] = __builtin_bit_cast(bf16x8, v);
-      }
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < RT; ++n)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, raw[X + 2 * n + h]),
+                                                                __builtin_bit_cast(bf16x8, raw[2 * m + h]), acc[m][n],
+                                                                0, 0, 0);
+      if (k + LORA_DOWN < c1) read(k + LORA_DOWN);
+      continue;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < L; ++i) *reinterpret_cast<lora_piece*>(mine + 64 * i + put) = raw[i];
+    lora_in_order();
+    if (k + LORA_DOWN < c1) read(k + LORA_DOWN);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const uint4* const from = mine + 8 * c + ((4 * h + g) ^ (c & 7));
+      bf16x8 af[RT];
+#pragma unroll
+      for (int n = 0; n < RT; ++n) af[n] = *reinterpret_cast<const bf16x8*>(from + 64 * X + 128 * n);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const bf16x8 xf = *reinterpret_cast<const bf16x8*>(from + 128 * m);
 #pragma unroll
         for (int n = 0; n < RT; ++n)
-          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[h][n], xf[h][m], acc[m][n], 0, 0, 0);
-  };
-  const int full = min(c1, pieces >> 3);
-  int k = c0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (; k < full; k += LORA_DOWN) chunk(k, std::true_type{});
-  for (; k < c1; k += LORA_DOWN) chunk(k, std::false_type{});
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[n], xf, acc[m][n], 0, 0, 0);
+      }
+    }
+    lora_in_order();
+  }
 }
 
 // v of a tile's tokens: .y = part of K, .z = group of 64 ranks.  The wavefronts take the part's chunks of 64 columns
 // in turn and join in LDS, pair by pair.
 template <bool GROUPED>
-__global__ __launch_bounds__(64 * LORA_DOWN, 2) void k_lora_down(LoraArgs a) {
+__global__ __launch_bounds__(64 * LORA_DOWN, GROUPED ? 2 : 4) void k_lora_down(LoraArgs a) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = blockIdx.y, r0 = blockIdx.z * (16 * LORA_RT);
   const int c0 = part * a.part_chunks, c1 = min(c0 + a.part_chunks, (a.K + 63) >> 6);
   constexpr int MT = GROUPED ? 4 : 1;
-  __shared__ f32x4 join[LORA_DOWN / 2][MT][LORA_RT][64];
+  __shared__ uint4 lines[LORA_DOWN][(MT + LORA_RT) * 128];
+  uint4* const mine = lines[w];
+  // the sums of half of the wavefronts, where the lines were
+  static_assert(sizeof(lines) >= sizeof(f32x4) * (LORA_DOWN / 2) * MT * LORA_RT * 64, "room for the sums");
+  f32x4 (*const join)[MT][LORA_RT][64] = reinterpret_cast<f32x4 (*)[MT][LORA_RT][64]>(&lines[0][0]);
   lora_tiles<GROUPED>(a, [&](const auto& tile) __attribute__((always_inline)) {
     if (tile.adapter < 0) return;
     const int rank = tile.rank;
     const int tiles = min((rank - r0 + 15) >> 4, LORA_RT), mt = (tile.rows + 15) >> 4;
     if (tiles <= 0) return;
+    __syncthreads();                             // the sums of the block's last tile have been read
     f32x4 acc[MT][LORA_RT];
     if (!GROUPED || mt == 1) {
-      if (tiles == 1) lora_rows<1, 1>(a, tile, rank, r0, c0, c1, acc);
-      else if (tiles == 2) lora_rows<1, 2>(a, tile, rank, r0, c0, c1, acc);
-      else lora_rows<1, 4>(a, tile, rank, r0, c0, c1, acc);
+      if (tiles == 1) lora_rows<1, 1, GROUPED>(a, tile, rank, r0, c0, c1, acc, mine);
+      else if (tiles == 2) lora_rows<1, 2, true>(a, tile, rank, r0, c0, c1, acc, mine);
+      else lora_rows<1, 4, true>(a, tile, rank, r0, c0, c1, acc, mine);
     } else if constexpr (GROUPED) {
-      if (tiles == 1) lora_rows<4, 1>(a, tile, rank, r0, c0, c1, acc);
-      else if (tiles == 2) lora_rows<4, 2>(a, tile, rank, r0, c0, c1, acc);
-      else lora_rows<4, 4>(a, tile, rank, r0, c0, c1, acc);
+      if (tiles == 1) lora_rows<4, 1, true>(a, tile, rank, r0, c0, c1, acc, mine);
+      else if (tiles == 2) lora_rows<4, 2, true>(a, tile, rank, r0, c0, c1, acc, mine);
+      else lora_rows<4, 4, true>(a, tile, rank, r0, c0, c1, acc, mine);
     }
 #pragma unroll
     for (int step = LORA_DOWN / 2; step; step >>= 1) {
@@ -321,52 +363,55 @@ __global__ __launch_bounds__(64 * LORA_DOWN, 2) void k_lora_down(LoraArgs a) {
   });
 }
 
-// The columns n0 .. n0 + 63 of a tile's tokens, MT tiles of 16 of them, by one wavefront of a block that has called
-// it with its others.  v goes to LDS in two bf16 values, upper halves and what is left of them; the weights come
-// straight from memory, and are on their way with the base rows before v is there.  16 ranks an instruction: lanes
-// of g = 0, 1 have the upper halves, g = 2, 3 the rest, of the same weights.  Lane: token c of a tile of 16, columns
-// 16 g .. +15 (row 4 g + i of matrix tile j is column 16 g + 4 j + i).
-template <int MT, typename Tile>
-__device__ __forceinline__ void lora_columns(const LoraArgs& a, const Tile& tile, int n0, uint4* vl) {
-  constexpr int RG = 2;            // steps of 16 ranks whose weights are read at once
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+// The columns n0 .. n0 + 63 of a tile's tokens from m0 on, MT tiles of 16 of them, by one wavefront of a block that
+// has called it with all of its NW.  v goes to LDS in two bf16 values, upper halves and what is left of them.  The weights of 32
+// ranks at a time, and at the end the sums of 16 tokens, go through LDS of the wavefront's own (`mine`, 4 KB): memory
+// is read and written in runs of 64 and 128 bytes, the matrix unit wants 16 rows in neighbouring lanes (with its
+// order in memory too 4096 tokens took 24 us).  16 ranks an instruction: lanes of g = 0, 1 have the upper halves,
+// g = 2, 3 the rest, of the same weights.  The many rows of a sorted call go around the caches, which the tokens' v
+// and x then stay in (8000 tokens of 2048 columns to 2048, rank 64: both products 46.3 and 42.4 us).
+template <int MT, int NW, typename Tile>
+__device__ __forceinline__ void lora_columns(const LoraArgs& a, const Tile& tile, int n0, int m0, uint4* vl,
+                                             uint4* mine) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, lr = lane >> 3, lp = lane & 7;
   const int rank = tile.rank, rows = tile.rows;
   const float scale = a.scales ? a.scales[tile.adapter] : 1.0f;
   const int pitch = a.vr / 8 + 1;                // of half a row, in pieces of 8; odd: rows fall to different banks
-  const uint16_t* const bt = a.b + (static_cast<int64_t>(tile.adapter) * a.N) * a.R;
-  const uint16_t* bp[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    bp[j] = bt + static_cast<int64_t>(min(n0 + 16 * (c >> 2) + 4 * j + (c & 3), a.N - 1)) * a.R;
-  uint4 bq[RG][4];
+  // weights: lane / 4 of 16 rows, piece lane % 4 of 8 ranks; what they hold past the rank does not matter
+  const uint16_t* const bt = a.b + static_cast<int64_t>(tile.adapter) * a.N * a.R;
+  lora_piece raw[4];
   auto read_b = [&](int r0) __attribute__((always_inline)) {
+    const int rr = r0 + 8 * (lane & 3), left = rank - rr;
+    auto keep = [&](int e) { return static_cast<int>((left > e ? 0xFFFFu : 0u) | (left > e + 1 ? 0xFFFF0000u : 0u)); };
+    const lora_piece kept{keep(0), keep(2), keep(4), keep(6)};
 #pragma unroll
-    for (int s = 0; s < RG; ++s) {
-      if (r0 + 16 * s >= rank) continue;
-      const int rr = r0 + 16 * s + 8 * (g & 1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bq[s][j] = *reinterpret_cast<const uint4*>(bp[j] + (rr < rank ? rr : 0));
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = min(n0 + 16 * j + (lane >> 2), a.N - 1);
+      raw[j] = *reinterpret_cast<const lora_piece*>(bt + n * a.R + (left > 0 ? rr : 0)) & kept;
     }
   };
-  read_b(0);
-  int t[MT];
-  uint4 old[MT][2];
+  if (rank) read_b(0);
+  // rows of base and out: 8 at a time, 8 lanes each
+  int t[MT][2];
+  lora_piece old[MT][2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    t[m] = static_cast<int>(tile.token(a, 16 * m + c));
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      old[m][h] = *reinterpret_cast<const uint4*>(a.base + t[m] * a.base_stride + min(n0 + 16 * g + 8 * h, a.N - 8));
-  }
+    for (int h = 0; h < 2; ++h) {
+      t[m][h] = static_cast<int>(tile.token(a, m0 + 16 * m + 8 * h + lr));
+      const auto* const p =
+          reinterpret_cast<const lora_piece*>(a.base + t[m][h] * a.base_stride + min(n0 + 8 * lp, a.N - 8));
+      old[m][h] = MT > 1 ? __builtin_nontemporal_load(p) : *p;
+    }
   // v: 2^sh pieces of a row, of which (rank + 7) / 8 are there
   const int per = (rank + 7) >> 3, sh = per > 1 ? 32 - __builtin_clz(per - 1) : 0;
   __syncthreads();                               // the previous tile's rows have been read
-  for (int e = threadIdx.x; e < rows << sh; e += 64 * LORA_UP) {
+  for (int e = threadIdx.x; e < rows << sh; e += 64 * NW) {
     const int row = e >> sh, piece = e & ((1 << sh) - 1);
     if (piece >= per) continue;
     const float* v = a.v + tile.token(a, row) * a.vr + 8 * piece;
     f32x4 s0 = {}, s1 = {};
-#pragma unroll 4
+#pragma unroll 2
     for (int p = 0; p < a.parts; ++p, v += a.T * a.vr) {
       s0 += *reinterpret_cast<const f32x4*>(v);
       s1 += *reinterpret_cast<const f32x4*>(v + 4);
@@ -382,79 +427,92 @@ __device__ __forceinline__ void lora_columns(const LoraArgs& a, const Tile& tile
     vl[(2 * row + 1) * pitch + piece] = __builtin_bit_cast(uint4, lo);
   }
   __syncthreads();
-  if (n0 >= a.N) return;
+  if (n0 >= a.N || m0 >= rows) return;
   f32x4 acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{};
-  for (int r0 = 0; r0 < rank; r0 += 16 * RG) {
-    if (r0) read_b(r0);
+  // rows of 4 pieces; piece p of row r at p ^ (r / 2 & 3): 8 rows of an operand fall to different banks
+  const int put = lane ^ (lane >> 3 & 3);
+  for (int r0 = 0; r0 < rank; r0 += 32) {
 #pragma unroll
-    for (int s = 0; s < RG; ++s) {
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<lora_piece*>(mine + 64 * j + put) = raw[j];
+    lora_in_order();
+    if (r0 + 32 < rank) read_b(r0 + 32);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
       if (r0 + 16 * s >= rank) continue;
       const int rr = r0 + 16 * s + 8 * (g & 1);
-      const int left = rank - rr;                // what the weights hold past the rank does not matter
-      if (r0 + 16 * s + 16 > rank) {
-        auto keep = [&](int e) { return (left > e ? 0xFFFFu : 0u) | (left > e + 1 ? 0xFFFF0000u : 0u); };
-        const uint32_t k0 = keep(0), k1 = keep(2), k2 = keep(4), k3 = keep(6);
+      bf16x8 bf[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bq[s][j].x &= k0;
-          bq[s][j].y &= k1;
-          bq[s][j].z &= k2;
-          bq[s][j].w &= k3;
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        bf[j] = *reinterpret_cast<const bf16x8*>(mine + 64 * j + 4 * c + ((2 * s + (g & 1)) ^ (c >> 1 & 3)));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint4 v = vl[(2 * min(16 * m + c, rows - 1) + (g >> 1)) * pitch + (rr < rank ? rr >> 3 : 0)];
+        uint4 v = vl[(2 * min(m0 + 16 * m + c, rows - 1) + (g >> 1)) * pitch + (rr < rank ? rr >> 3 : 0)];
         if (rr >= rank) v = uint4{};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bq[s][j]),
-                                                              __builtin_bit_cast(bf16x8, v), acc[m][j], 0, 0, 0);
+          acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], __builtin_bit_cast(bf16x8, v), acc[m][j], 0, 0, 0);
       }
     }
+    lora_in_order();
   }
+  // lane: columns 16 j + 4 g .. +3 of token c, which is piece 4 j + g of row c, at that ^ c
+  const int n = n0 + 8 * lp;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (16 * m + c >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(mine + 16 * c + ((4 * j + g) ^ c)) = acc[m][j];
+    lora_in_order();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int n = n0 + 16 * g + 8 * h;
-      if (n >= a.N) continue;
-      const uint32_t u[4] = {old[m][h].x, old[m][h].y, old[m][h].z, old[m][h].w};
-      uint32_t o[4];
+      const int r = 8 * h + lr;
+      const f32x4 s0 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp) ^ r));
+      const f32x4 s1 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp + 1) ^ r));
+      lora_piece o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const f32x4& s = acc[m][2 * h + (e >> 1)];
-        o[e] = pack_bf16x2(fmaf(scale, s[2 * (e & 1)], __uint_as_float(u[e] << 16)),
-                           fmaf(scale, s[2 * (e & 1) + 1], __uint_as_float(u[e] & 0xFFFF0000u)));
+        const f32x4& s = e < 2 ? s0 : s1;
+        const uint32_t u = static_cast<uint32_t>(old[m][h][e]);
+        o[e] = static_cast<int>(pack_bf16x2(fmaf(scale, s[2 * (e & 1)], __uint_as_float(u << 16)),
+                                            fmaf(scale, s[2 * (e & 1) + 1], __uint_as_float(u & 0xFFFF0000u))));
       }
-      *reinterpret_cast<uint4*>(a.out + t[m] * a.out_stride + n) = uint4{o[0], o[1], o[2], o[3]};
+      if (m0 + 16 * m + r < rows && n < a.N) {
+        auto* const p = reinterpret_cast<lora_piece*>(a.out + t[m][h] * a.out_stride + n);
+        if (MT > 1) __builtin_nontemporal_store(o, p);
+        else *p = o;
+      }
     }
+    lora_in_order();
   }
 }
 
-// Rows of the output: .y = 256 columns, 64 a wavefront.
+// Rows of the output: .y = 256 columns, 64 a wavefront; grouped, the second four wavefronts have the tokens from 32 on
+// (4096 tokens of 4096 columns, rank 32: 21.0 us, and 23.3 with all 64 in each of four wavefronts, of which a CU then
+// has 12 in place of 16; several strips of columns in turn, the next one's base on its way: 29 us).
 template <bool GROUPED>
-__global__ __launch_bounds__(64 * LORA_UP, GROUPED ? 3 : 4) void k_lora_up(LoraArgs a) {
+__global__ __launch_bounds__(64 * LORA_UP * (GROUPED ? 2 : 1), 4) void k_lora_up(LoraArgs a) {
+  constexpr int NW = LORA_UP * (GROUPED ? 2 : 1);
+  __shared__ uint4 turn[NW][256];
   extern __shared__ uint4 vl[];                  // [tokens of a tile: 64 grouped, else 16][2 halves][pitch] pieces of 8 values
-  const int n0 = blockIdx.y * (64 * LORA_UP) + 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint4* const mine = turn[w];
+  const int n0 = blockIdx.y * (64 * LORA_UP) + 64 * (w % LORA_UP), m0 = w / LORA_UP * 32;
   lora_tiles<GROUPED>(a, [&](const auto& tile) __attribute__((always_inline)) {
     if (tile.adapter < 0) {                      // base as it is, 8 tokens at a time
       const int lane = threadIdx.x & 63, n = n0 + 8 * (lane & 7);
       if (a.out == a.base || n >= a.N) return;
-      for (int i = lane >> 3; i < tile.rows; i += 8) {
+      for (int i = m0 + (lane >> 3); i < min(tile.rows, GROUPED ? m0 + 32 : 64); i += 8) {
         const int64_t t = tile.token(a, i);
         *reinterpret_cast<uint4*>(a.out + t * a.out_stride + n) =
             *reinterpret_cast<const uint4*>(a.base + t * a.base_stride + n);
       }
-    } else if (!GROUPED || tile.rows <= 16) {
-      lora_columns<1>(a, tile, n0, vl);
     } else if constexpr (GROUPED) {
-      lora_columns<4>(a, tile, n0, vl);
+      lora_columns<2, NW>(a, tile, n0, m0, vl, mine);
+    } else {
+      lora_columns<1, NW>(a, tile, n0, m0, vl, mine);
     }
   });
 }

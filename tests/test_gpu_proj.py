@@ -240,6 +240,15 @@ def test_lora_strides(in_place):
     lora_case(70, 128, 264, 32, 5, mixed(70, 5, 2), 2, scales=False, in_place=in_place)
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128, 200, 256])
+def test_lora_ranks_of_sorted_calls(R):
+    """More than 64 tokens: tiles of up to 16 and of up to 64 of them, ranks in up to four groups of 64."""
+    n = 5
+    ids = np.concatenate([np.full(70, 0), np.full(9, 1), mixed(81, n, R)])
+    lora_case(160, 264, 280, R, n, ids, R, ranks=[R, max(1, R - 3), 1, 0, R // 2 + 1], what="sorted")
+    lora_case(160, 1096, 72, R, n, ids, R + 1, in_place=True, what="sorted, in place")
+
+
 @pytest.mark.parametrize("n", [511, 512, 700])
 @pytest.mark.parametrize("T", [1, 64, 65, 200, 330])
 def test_lora_many_adapters(T, n):
