@@ -52,23 +52,25 @@ int fp8_few(const Fp8Args& a, hipStream_t s) {
   return launch(k_proj_fp8_few<NT, MT, 8, U>, grid, dim3(512), s, a);
 }
 
-template <int WN, int WT, int TT>
+template <int WN, int WT, int TT, int SLOTS>
 int fp8_tile(const Fp8Args& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(cdiv(cdiv(a.N, 64 * WN) * cdiv(a.T, 16 * TT * WT), 8) * 8));
-  return launch(k_proj_fp8_tile<WN, WT, 4, TT>, grid, dim3(64 * WN * WT), s, a);
+  return launch(k_proj_fp8_tile<WN, WT, 4, TT, SLOTS>, grid, dim3(64 * WN * WT), s, a);
 }
 
 // The smallest blocks that the 256 CUs take at once, one each: a block's time is that of
 // its chain of reads (4096 columns; blocks of 16 x 16, 32 x 16, 32 x 32, 64 x 32, 64 x 64
 // outputs x tokens, tiles of 128 x 128; us, those not shown are slower):
 //   1 token to 1024: 3.8, 4.5; 64 to 2048: 5.9, 5.7, 6.5; 32 to 6144: 9.5, 9.3, 8.4, 9.3;
-//   64 to 6144: -, 12.3, 11.1, 9.9, 12.9; 128 to 6144: -, 19.4, 15.5, 16.3, 13.1, 24.7.
+//   64 to 6144: -, 12.3, 11.1, 9.9, 12.9; 128 to 6144: -, 19.4, 15.5, 16.3, 13.1, 22.
 // Up to 16 tokens the weights' stream is all there is, and small blocks may share a CU
 // (to 6144: 7.1, 7.4; to 12288: 10.7, 11.9; 2048 to 16384: 10.0, 7.8).  Past one block of
-// 64 x 64 a CU, up to five of 32 x 32 (700 to 1536: -, -, 19.1, 21.9, 22.7, 24.8; 300 to
-// 4096: -, -, 20.8, 22.5, 23.0, 24.2; 384 to 6144, nine of them: -, -, 34.6, 36.5, 33.8,
-// 25.3), then tiles of 128 x 128 while their blocks, two a CU, have places at once, and
-// of 256 x 256 after that (2048 to 4096: 39 and 52 us; 1536 to 6144: 58 and 53 us).
+// 64 x 64 a CU, up to five of 32 x 32 (700 to 1536: -, -, 19.5, 22.3, 23.1, 21.9; 300 to
+// 4096: -, -, 22.0, 23.7, 23.3, 21.8; 384 to 6144, nine of them: -, -, 38.4, 37.5, 34.3,
+// 22.8), then tiles of 128 x 128, with four slots while each has a CU to itself (512 to
+// 6144: 23.4 us, 25.9 with two slots) and two while two a CU have places at once (2048
+// to 4096: 49 and 38 us), and of 256 x 256 after that (2048 to 4096 48, 4096 to 6144 104
+// and 107 us).
 int fp8(const Fp8Args& a, hipStream_t s) {
   auto blocks = [&](int n, int t) { return cdiv(a.N, n) * cdiv(a.T, t); };
   if (blocks(16, 16) <= (a.T <= 16 ? 768 : 256)) return fp8_few<1, 1, 4>(a, s);
@@ -77,8 +79,9 @@ int fp8(const Fp8Args& a, hipStream_t s) {
   if (blocks(64, 32) <= 256) return fp8_few<4, 2, 1>(a, s);
   if (blocks(64, 64) <= 256) return fp8_few<4, 4, 1>(a, s);
   if (blocks(32, 32) <= 5 * 256) return fp8_few<2, 2, 2>(a, s);
-  if (blocks(128, 128) <= 512) return fp8_tile<2, 2, 4>(a, s);
-  return fp8_tile<4, 2, 8>(a, s);
+  if (blocks(128, 128) <= 256) return fp8_tile<2, 2, 4, 4>(a, s);
+  if (blocks(128, 128) <= 512) return fp8_tile<2, 2, 4, 2>(a, s);
+  return fp8_tile<4, 2, 8, 2>(a, s);
 }
 
 // How the adapters' products are cut.

@@ -167,7 +167,7 @@ __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
 
 // Many tokens: tiles of 16 NJ WN weight rows x 16 TT WT tokens, one a block of
 // WN x WT wavefronts with 16 NJ x 16 TT each.  Spans of both operands go to LDS by
-// DMA, two slots.
+// DMA, SLOTS - 1 of them ahead.
 //   * A slot's row has 8 pieces of 16 bytes; piece p of row r is at place p ^ (r & 7),
 //     so that the 16 rows of a fragment, 128 bytes apart, fall to different banks.
 //   * Each 64 weight rows are in the order in which a lane ends with 16 neighbouring
@@ -175,26 +175,33 @@ __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
 //     16 g + 4 j + i, and lane (g, token) has elements i of tiles j.
 //   * The scales of the tokens come in groups of 4 spans, 64 tokens a transfer (a load
 //     of its own by each wavefront for each span: 184 us where this took 117).
-//   * There is one barrier a span; the next span's transfers are spread over the
-//     products behind it.  (A barrier before the last products, which then hide the
-//     reads of the next span's first fragments: no faster, for 20 registers more.)
+//   * There is one barrier a span; the transfers are spread over the products behind
+//     it.
 //   * Transfers past the last row bring zeros (bounds of the buffer).
-// Measured, 4096 tokens of 4096 columns to 6144: 117-125 us in tiles of 256 x 256,
-// 1.65-1.76 PFLOP/s, where a large library product of E4M3 with one scale in all
-// reaches 2.3 (this size) to 3.0.  The chip is at its power limit then: without the
-// transfers and the scales it takes 90 us with all CUs and 35 us a round with nine,
-// not twice as long.  The fmas take 9% of the time, the transfers 13%, the reads of
-// LDS 25%.  Wavefronts of 128 x 128, one a SIMD, do not keep the matrix unit busy
-// (163 us); instructions of 32 x 32 over half a span need more registers for the
-// sums of a span (131-139 us).
-template <int WN, int WT, int NJ, int TT>
-__global__ __launch_bounds__(64 * WN * WT, WN * WT > 4 || NJ * TT <= 16 ? 2 : 1) void k_proj_fp8_tile(Fp8Args a) {
+// What bounds it: a CU brings about 48 GB/s from outside its L2, whatever the tile
+// (4096 columns: a block of 128 x 128, 1 MB, 22 us, of 256 x 256, 2 MB, 44 us, alone
+// on its CU), so the largest tiles that still fill the GPU are the fastest.  Four slots
+// where a CU has one block: 512 tokens to 6144 23.4 us, and 25.9 with two; reading the
+// next span's first fragments before its barrier as well: 23.7.
+// 4096 tokens of 4096 columns to 6144: 102-105 us one after the other (117 with pauses,
+// as a profiler makes them) in tiles of 256 x 256, 2.0 PFLOP/s, where a large library
+// product of E4M3 with one scale in all reaches 2.3 (this size) to 3.0.  The chip is at
+// its power limit then: without the transfers and the scales it takes 90 us with all
+// CUs and 35 us a round with nine, not twice as long.  The fmas take 9% of the time,
+// the transfers 13%, the reads of LDS 25%.  Wavefronts of 128 x 128, one a SIMD, do not
+// keep the matrix unit busy (163 us); instructions of 32 x 32 over half a span need
+// more registers for the sums of a span (131-139 us).
+template <int WN, int WT, int NJ, int TT, int SLOTS>
+__global__ __launch_bounds__(64 * WN * WT, SLOTS > 2 ? 1 : 2) void k_proj_fp8_tile(Fp8Args a) {
   constexpr int NW = WN * WT, BN = 16 * NJ * WN, BT = 16 * TT * WT;
   constexpr int IW = BN * 8 / 64 / NW, IX = BT * 8 / 64 / NW;     // transfers of a wavefront a span
   constexpr int SPREAD = 4, LAG = 3;                         // products between one and its fmas
   static_assert(BN * 8 % (64 * NW) == 0 && BT * 8 % (64 * NW) == 0, "whole transfers");
   static_assert(BT % 64 == 0 && BT / 64 <= NW, "scales: 64 tokens a wavefront");
+  static_assert(SLOTS == 2 || SLOTS == 4, "slots in turn");
+  constexpr int MORE = SLOTS > 2 ? 1 : 0;
   __shared__ uint4 w0[BN * 8], w1[BN * 8], x0[BT * 8], x1[BT * 8], xsl[2 * BT];
+  __shared__ uint4 w2[MORE * BN * 8 + 1], w3[MORE * BN * 8 + 1], x2[MORE * BT * 8 + 1], x3[MORE * BT * 8 + 1];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wv % WN, wt = wv / WN;
   const int n_tiles = (a.N + BN - 1) / BN, spans = a.K >> 7;
@@ -241,10 +248,11 @@ __global__ __launch_bounds__(64 * WN * WT, WN * WT > 4 || NJ * TT <= 16 ? 2 : 1)
     if (wv < BT / 64) bring(sbase, sbytes, (64 * wv + lane) * spans * 4, 16 * q, xsl + (q & 1) * BT + 64 * wv);
   };
   const float* const wscale = a.ws + static_cast<int64_t>(min(n0 + 16 * NJ * wn, a.N - 1) >> 7) * spans;
-  // this wavefront's transfers have come, and everyone is here
+  // this wavefront's transfers of the span have come (those of the spans behind it may be on their way), and everyone
+  // is here
   auto arrive = [&]() __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((SLOTS - 2) * (IW + IX)));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -278,13 +286,13 @@ __global__ __launch_bounds__(64 * WN * WT, WN * WT > 4 || NJ * TT <= 16 ? 2 : 1)
   auto span = [&](int s, const uint4* wl, const uint4* xl, uint4* wnext, uint4* xnext) __attribute__((always_inline)) {
     constexpr int M = NJ * TT, I = IW + IX, SP = M / SPREAD;
     arrive();
-    const int next = min(s + 1, spans - 1);      // past the end the last span again, which nobody reads
+    const int next = min(s + SLOTS - 1, spans - 1);      // past the end the last span again, which nobody reads
     read_x(xl, 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) read_w(wl, j);
 #pragma unroll
     for (int t = 0; t < TT; ++t) scale[t] = read_scale(s, t) * ws;
-    ws = wscale[next];                           // ahead of the transfers, so that nothing waits for those
+    ws = wscale[min(s + 1, spans - 1)];          // ahead of the transfers, so that nothing waits for those
     if ((s & 3) == 0) issue_scales((s >> 2) + 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -301,14 +309,28 @@ __global__ __launch_bounds__(64 * WN * WT, WN * WT > 4 || NJ * TT <= 16 ? 2 : 1)
 #pragma unroll
     for (int m = M - LAG; m < M; ++m) add(m);
   };
-  issue(0, w0, x0);
   issue_scales(0);
+  issue(0, w0, x0);
   int s = 0;
-  for (; s + 1 < spans; s += 2) {
-    span(s, w0, x0, w1, x1);
-    span(s + 1, w1, x1, w0, x0);
+  if constexpr (SLOTS == 2) {
+    for (; s + 1 < spans; s += 2) {
+      span(s, w0, x0, w1, x1);
+      span(s + 1, w1, x1, w0, x0);
+    }
+    if (s < spans) span(s, w0, x0, w1, x1);
+  } else {
+    issue(min(1, spans - 1), w1, x1);
+    issue(min(2, spans - 1), w2, x2);
+    for (; s + 3 < spans; s += 4) {
+      span(s, w0, x0, w3, x3);
+      span(s + 1, w1, x1, w0, x0);
+      span(s + 2, w2, x2, w1, x1);
+      span(s + 3, w3, x3, w2, x2);
+    }
+    if (s < spans) span(s, w0, x0, w3, x3);
+    if (s + 1 < spans) span(s + 1, w1, x1, w0, x0);
+    if (s + 2 < spans) span(s + 2, w2, x2, w1, x1);
   }
-  if (s < spans) span(s, w0, x0, w1, x1);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));      // transfers end before the block gives up its LDS
 #pragma unroll
   for (int q = 0; q < NJ / 4; ++q) {
