@@ -15,6 +15,12 @@
 //
 // The prefix may end inside a page, and inside a tile: the rest of its last tile is
 // masked there, and the keys before its end in the first own tile.
+//
+// What bounds it: few rows behind a short prefix, two launches (4 sequences behind
+// 1024 keys, 32/8 heads of 128 dims: 10.4 us); many behind a long one, the prefix's
+// products and bytes, then the own keys' bytes, then the parts' sums, one after the
+// other (64 sequences behind 32768 keys with up to 1024 of their own: 46, 33 and 10
+// us; with up to 256 of their own 62 us in all, and 498 us by moe_attn_decode).
 #pragma once
 
 #include "attn.hpp"

@@ -19,7 +19,7 @@
 // (adapter numbers, weights, parts); with many the rows, x once and base in and out
 // once, at two thirds of a copy's rate, and the sort.  4096 columns: one token of
 // rank 16 to 6144 10 us (5.0 and 5.6 in the kernels), 64 tokens of 32 adapters of
-// rank 64 to 6144 17 us (7.5 and 9.3: 3.2 TB/s), 4096 tokens of 5 adapters of rank 32
+// rank 64 to 6144 17 us (7.5 and 9.3), 4096 tokens of 5 adapters of rank 32
 // to 4096 38 us (sort 7.0, 12.2 for 34 MB and 19.5 for 67 MB).
 #pragma once
 

@@ -3,7 +3,8 @@
 //   h = x + r;  y = h rsqrt(mean(h^2) + eps) w;  per 128 columns s = max|y| / 448, q = e4m3(y / s)
 //
 // What bounds it: every value is read and written once, for a dozen operations;
-// with few rows, the launch.  So a row is read into registers, WPR wavefronts of
+// with few rows, the launch (4096 columns, all outputs: 4096 rows 28.8 us, 5.2 TB/s, a
+// copy's rate; one row 2.7 us).  So a row is read into registers, WPR wavefronts of
 // NV pieces of 8 values a lane, its squares are summed (over the wavefronts in
 // LDS), and everything that is asked for goes out from there.  16 neighbouring
 // lanes hold the 128 columns of a scale.
@@ -40,7 +41,8 @@ __device__ __forceinline__ float row_max(float v) {
   return dpp_max(v, dpp_mov<DPP_ROW_MIRROR>(__float_as_int(v)));
 }
 
-// Rows that are read once go around the caches (4096 x 4096: 36 us with ordinary loads, 32 us with these).
+// Rows that are read once go around the caches (4096 x 4096, two pieces a lane:
+// 36 us with ordinary loads, 32 us with these).
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
