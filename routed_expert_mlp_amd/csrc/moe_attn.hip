@@ -214,10 +214,9 @@ PrefillPlan prefill_plan(const moe_attn_config* c, int64_t T, int64_t B, int64_t
 // tiles of 32 keys, two blocks a CU, of which one starts or ends while the other
 // computes.  Long blocks that fill the GPU for 16 tiles want the former (32/8
 // heads: 4096 tokens 130 us, and 144 us with 4; 512 tokens behind 65024 466 and
-// 533 us, behind 3072 41.4 and 44.5 us), short or few ones the latter (2048 tokens
-// 48 us, and 51 us with 8; a window of 1024 on 8192 tokens 151 and 159 us; 256
-// tokens behind 3072 27.3 and 29.5 us; 16 behind 8176 16.3 and 19.5 us).  Other widths
-// have one form.
+// 533 us), short or few ones the latter (2048 tokens 48 us, and 51 us with 8; a
+// window of 1024 on 8192 tokens 151 and 159 us; 16 behind 8176 16.3 and 19.5 us).
+// Other widths have one form.
 template <typename F>
 int with_prefill_shape(const moe_attn_config* c, int64_t T, int64_t B, int64_t max_q, int64_t max_len, F&& f) {
   using four = std::integral_constant<int, 4>;
