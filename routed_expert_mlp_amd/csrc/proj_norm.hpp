@@ -3,8 +3,8 @@
 //   h = x + r;  y = h rsqrt(mean(h^2) + eps) w;  per 128 columns s = max|y| / 448, q = e4m3(y / s)
 //
 // What bounds it: every value is read and written once, for a dozen operations;
-// with few rows, the launch (4096 columns, all outputs: 4096 rows 28.8 us, 5.2 TB/s, a
-// copy's rate; one row 2.7 us).  So a row is read into registers, WPR wavefronts of
+// with few rows, the launch (4096 columns, all outputs: 4096 rows 27.4 us, 5.5 TB/s, a
+// copy's rate; one row 2.5 us).  So a row is read into registers, WPR wavefronts of
 // NV pieces of 8 values a lane, its squares are summed (over the wavefronts in
 // LDS), and everything that is asked for goes out from there.  16 neighbouring
 // lanes hold the 128 columns of a scale.
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_proj_norm(NormArg
   const int pieces = a.hidden / 8;
   const uint4* const x = reinterpret_cast<const uint4*>(a.x + t * a.x_stride);
   const int64_t row = t * pieces;
-  float v[NV][8];
+  float v[NV][8], weight[NV][8];
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -137,6 +137,16 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_proj_norm(NormArg
     uint4 raw = {}, res = {};
     if (in) raw = load_once(x + p);
     if (in && a.r) res = load_once(reinterpret_cast<const uint4*>(a.r) + row + p);
+    f32x4 w0{1.0f, 1.0f, 1.0f, 1.0f}, w1 = w0;   // on their way before the sum is there (4096 rows 28.8 us behind it)
+    if (in && a.w) {
+      w0 = reinterpret_cast<const f32x4*>(a.w)[2 * p];
+      w1 = reinterpret_cast<const f32x4*>(a.w)[2 * p + 1];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      weight[i][j] = w0[j];
+      weight[i][4 + j] = w1[j];
+    }
     bf16x8_to_f32(raw, v[i]);
     if (a.r) {
       float f[8];
@@ -162,24 +172,15 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_proj_norm(NormArg
     const int p = lane + LANES * i;
     const bool in = p < pieces;
     if (in && a.h) reinterpret_cast<uint4*>(a.h)[row + p] = f32_to_bf16x8(v[i]);
-    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-    if (in && a.w) {
-      const f32x4 w0 = reinterpret_cast<const f32x4*>(a.w)[2 * p], w1 = reinterpret_cast<const f32x4*>(a.w)[2 * p + 1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = w0[j];
-        w[4 + j] = w1[j];
-      }
-    }
     if (in && a.y) {
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = v[i][j] * (inv * w[j]);
+      for (int j = 0; j < 8; ++j) y[j] = v[i][j] * (inv * weight[i][j]);
       reinterpret_cast<uint4*>(a.y)[row + p] = f32_to_bf16x8(y);
     }
     if (a.q) {
       E4m3Block q;
-      q.products(v[i], w);             // lanes past the row's end have zeros
+      q.products(v[i], weight[i]);            // lanes past the row's end have zeros
       const float s = fmaxf(q.top * inv * (1.0f / 448.0f), 1.17549435e-38f);
       if (in) {
         reinterpret_cast<uint2*>(a.q)[row + p] = q.codes(inv, s);
