@@ -92,6 +92,11 @@ struct LoraPlan {
   size_t tiles_at, count_at, order_at, ws_bytes;     // in the workspace, behind v
 };
 
+// Every tile of a window reads its adapter again, and the sort is a launch more, of 4 to 10 us: as many tiles are read
+// in less (4096 columns to 4096, windows and sorted: 512 tokens of 3 adapters of rank 16 or 64, 56 tiles, 12.6 and 17.7,
+// 15.9 and 22.1 us; 1024 of them, 112 tiles, 20.9 and 19.9, 27.2 and 27.6; 128 tokens of 32, 72 tiles, 14.2 and 16.0,
+// 20.5 and 20.3; 192 of them, 108 tiles, 19.6 and 15.8, 30.2 and 20.1).
+constexpr int64_t LORA_WINDOW_TILES = 80;
 constexpr int64_t LORA_BLOCKS = 256;      // blocks of k_lora_down with something to do
 
 LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
@@ -103,13 +108,14 @@ LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
   p.parts = cdiv(chunks, p.part_chunks);
   p.groups = static_cast<int>(cdiv(d->max_rank, 16 * LORA_RT));
   p.col_blocks = static_cast<int>(cdiv(d->out_features, 64 * LORA_UP));
-  p.grouped = T > 64 && d->n_adapters < LORA_BINS;
+  // windows of 64 tokens, and the most tiles of up to 16 tokens of an adapter in one
+  const int64_t windows = cdiv(T, 64), in = std::min<int64_t>(64, T), most = std::min(in, d->n_adapters + in / 16);
+  p.grouped = windows * most > LORA_WINDOW_TILES && d->n_adapters < LORA_BINS;
   // every adapter, and the tokens without one, leave at most one tile unfilled
   const int64_t tiles = T / 64 + std::min(T, d->n_adapters + 1);
   if (p.grouped) {
     p.down_x = p.up_x = tiles;
   } else {
-    const int64_t windows = cdiv(T, 64), in = std::min<int64_t>(64, T), most = std::min(in, d->n_adapters + in / 16);
     auto slots = [&](int64_t blocks) { return static_cast<int>(std::max<int64_t>(1, std::min(most, blocks))); };
     p.slots_down = slots(2048 / (windows * p.parts));
     p.slots_up = slots(4096 / (windows * p.col_blocks));

@@ -4,10 +4,10 @@
 //
 // The tokens of an adapter are gathered into the rows of a matrix product, 64 at a
 // time (a tile), in whatever order they come, so that an adapter is read once for
-// them.  Up to 64 tokens each block finds its adapter's tokens itself: every
+// them.  In windows of 64 tokens each block finds its adapter's tokens itself: every
 // wavefront reads the adapter numbers, one a lane, and lanes of one adapter find each
-// other with a ballot for each bit of its number.  With more, k_lora_group sorts the
-// tokens by adapter first (4096 tokens of 50 adapters in any order: 466 us in windows
+// other with a ballot for each bit of its number.  Where windows would read the
+// adapters too often, k_lora_group sorts the tokens by adapter first (4096 tokens of 50 adapters in any order: 466 us in windows
 // of 64 tokens, each of which reads most adapters again, and 51 us sorted).
 //
 // v is a sum over thousands of columns, cut into parts for the blocks; k_lora_up

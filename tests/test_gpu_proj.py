@@ -242,11 +242,19 @@ def test_lora_strides(in_place):
 
 @pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128, 200, 256])
 def test_lora_ranks_of_sorted_calls(R):
-    """More than 64 tokens: tiles of up to 16 and of up to 64 of them, ranks in up to four groups of 64."""
-    n = 5
+    """Tokens sorted by adapter: tiles of up to 16 and of up to 64 of them, ranks in up to four groups of 64."""
+    n = 40
     ids = np.concatenate([np.full(70, 0), np.full(9, 1), mixed(81, n, R)])
-    lora_case(160, 264, 280, R, n, ids, R, ranks=[R, max(1, R - 3), 1, 0, R // 2 + 1], what="sorted")
+    ranks = [R, max(1, R - 3), 1, 0, R // 2 + 1] * 8
+    lora_case(160, 264, 280, R, n, ids, R, ranks=ranks, what="sorted")
     lora_case(160, 1096, 72, R, n, ids, R + 1, in_place=True, what="sorted, in place")
+
+
+@pytest.mark.parametrize("T", [65, 127, 300, 513, 704, 705, 1000])
+def test_lora_windows_of_few_adapters(T):
+    """Several windows of 64 tokens, and from 705 on the same sorted."""
+    lora_case(T, 136, 264, 16, 3, mixed(T, 3, T), T, what="in any order")
+    lora_case(T, 72, 520, 72, 3, np.sort(mixed(T, 3, T)), T, ranks=[72, 5, 40], in_place=True, what="in runs")
 
 
 @pytest.mark.parametrize("n", [511, 512, 700])
