@@ -97,22 +97,25 @@ struct LoraPlan {
 // 15.9 and 22.1 us; 1024 of them, 112 tiles, 20.9 and 19.9, 27.2 and 27.6; 128 tokens of 32, 72 tiles, 14.2 and 16.0,
 // 20.5 and 20.3; 192 of them, 108 tiles, 19.6 and 15.8, 30.2 and 20.1).
 constexpr int64_t LORA_WINDOW_TILES = 80;
-constexpr int64_t LORA_BLOCKS = 256;      // blocks of k_lora_down with something to do
+// Blocks of k_lora_down: of a sorted call one a CU, 128 KB of LDS, its unfilled tiles counted too (as many parts as fill
+// 256 with full tiles alone, and this way: 4096 tokens of 50 adapters of rank 32 51 and 46 us, 2000 of 4 of rank 128 43 and 36 us, 200 of 60 of rank 32 27 and 23 us).
+constexpr int64_t LORA_BLOCKS = 256;
 
 LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
   LoraPlan p{};
   const int64_t chunks = cdiv(d->in_features, 64), vr = cdiv(d->max_rank, 16) * 16;
-  // parts of the sum over the input, for tiles of 64 tokens; none shorter than 8 chunks of 64 columns
-  const int64_t most_parts = cdiv(chunks, 8);
-  p.part_chunks = cdiv(chunks, std::max<int64_t>(1, std::min(most_parts, LORA_BLOCKS / cdiv(T, 64))));
-  p.parts = cdiv(chunks, p.part_chunks);
   p.groups = static_cast<int>(cdiv(d->max_rank, 16 * LORA_RT));
   p.col_blocks = static_cast<int>(cdiv(d->out_features, 64 * LORA_UP));
   // windows of 64 tokens, and the most tiles of up to 16 tokens of an adapter in one
   const int64_t windows = cdiv(T, 64), in = std::min<int64_t>(64, T), most = std::min(in, d->n_adapters + in / 16);
   p.grouped = windows * most > LORA_WINDOW_TILES && d->n_adapters < LORA_BINS;
-  // every adapter, and the tokens without one, leave at most one tile unfilled
+  // sorted, every adapter, and the tokens without one, leave at most one tile unfilled
   const int64_t tiles = T / 64 + std::min(T, d->n_adapters + 1);
+  // parts of the sum over the input; none shorter than 8 chunks of 64 columns
+  const int64_t most_parts = cdiv(chunks, 8);
+  const int64_t parts = LORA_BLOCKS / (p.grouped ? tiles * p.groups : windows);
+  p.part_chunks = cdiv(chunks, std::max<int64_t>(1, std::min(most_parts, parts)));
+  p.parts = cdiv(chunks, p.part_chunks);
   if (p.grouped) {
     p.down_x = p.up_x = tiles;
   } else {
@@ -122,7 +125,7 @@ LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
     p.down_x = windows * p.slots_down;
     p.up_x = windows * p.slots_up;
   }
-  // of T tokens or fewer: more than one part only while parts x tiles of 64 tokens are at most LORA_BLOCKS
+  // of T tokens or fewer: more than one part only while parts x full tiles of 64 tokens are at most LORA_BLOCKS
   const int64_t rows = std::min(T * most_parts, std::max<int64_t>(T, LORA_BLOCKS * 64));
   p.tiles_at = size_t(rows) * vr * 4;
   p.count_at = p.tiles_at + size_t(tiles) * 16;
