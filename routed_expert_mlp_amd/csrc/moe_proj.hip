@@ -98,7 +98,8 @@ struct LoraPlan {
 // 20.5 and 20.3; 192 of them, 108 tiles, 19.6 and 15.8, 30.2 and 20.1).
 constexpr int64_t LORA_WINDOW_TILES = 80;
 // Blocks of k_lora_down: of a sorted call one a CU, 128 KB of LDS, its unfilled tiles counted too (as many parts as fill
-// 256 with full tiles alone, and this way: 4096 tokens of 50 adapters of rank 32 51 and 46 us, 2000 of 4 of rank 128 43 and 36 us, 200 of 60 of rank 32 27 and 23 us).
+// 256 with full tiles alone, and this way: 4096 tokens of 50 adapters of rank 32 51 and 46 us, 2000 of 4 of rank 128 43
+// and 36 us, 200 of 60 of rank 32 27 and 23 us).
 constexpr int64_t LORA_BLOCKS = 256;
 
 LoraPlan lora_plan(const moe_proj_adapters* d, int64_t T) {
