@@ -133,8 +133,8 @@ __device__ __forceinline__ AttnTiles attn_tiles_between(const AttnArgs& a, int k
   return t;
 }
 
-// Positions of the new tokens of a batch that columns c0 .. c1 - 1 of a key/value head have: of this lane's column, and
-// the first and the last of all of them.
+// Positions of the new tokens of a batch that columns c0 .. c1 - 1 of a key/value head have: of this lane's column
+// (below 0: none, it sees nothing), and the first and the last of those that are positions (none: past all, and -1).
 struct AttnSpan {
   int pos, first, last;
 };
@@ -148,10 +148,10 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int col, int c0
   AttnSpan s;
   s.pos = attn_position(a, col / a.group);
   const int t0 = c0 / a.group, t1 = (c1 - 1) / a.group;
-  int lo = 0x7FFFFFFF, hi = -0x7FFFFFFF;
+  int lo = 0x7FFFFFFF, hi = -1;
   for (int t = t0 + static_cast<int>(threadIdx.x & 63); t <= t1; t += 64) {
     const int p = attn_position(a, t);
-    lo = min(lo, p);
+    lo = min(lo, p < 0 ? 0x7FFFFFFF : p);
     hi = max(hi, p);
   }
 #pragma unroll
@@ -185,6 +185,13 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
 // key <= p and (key >= lo or key < sinks).
 __device__ __forceinline__ uint64_t visible_bits(int key0, int p, int lo, int sinks) {
   return low_bits(p + 1 - key0) & (~low_bits(lo - key0) | low_bits(sinks - key0));
+}
+
+// Bits that a lane or more of each half of a wavefront has.
+__device__ __forceinline__ uint32_t or_of_half(uint32_t bits) {
+#pragma unroll
+  for (int x = 16; x; x >>= 1) bits |= __shfl_xor(bits, x);
+  return bits;
 }
 
 // x where bit `bit` of the mask is set, else -inf.

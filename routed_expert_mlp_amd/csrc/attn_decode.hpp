@@ -195,11 +195,15 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
       const uint32_t see = static_cast<uint32_t>(
           visible_bits(key0 + 8 * half, lead ? min(pos, a.shared - 1) : pos, attn_window_lo(a, pos), tl.sinks) &
           mine(key0 + 8 * half));
+      // a sequence's new tokens, or sequences that go on behind the prefix, see the keys from tl.lo on without a gap;
+      // windows that end inside the prefix may leave some, which only the columns together know
+      const bool gaps = lead && a.window && first < a.shared - 1;
+      const uint32_t any = gaps ? or_of_half(see) : 0;
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[e] = keep_if(see, 16 * (e >> 3) + (e & 7), sc[e]);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const uint4 mk = value_mask(static_cast<uint32_t>(
+        const uint4 mk = value_mask(gaps ? any >> (16 * g) : static_cast<uint32_t>(
             visible_bits(key0 + 16 * g + 8 * half, tl.hi - 1, tl.lo, tl.sinks) & mine(key0 + 16 * g + 8 * half)));
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) vf[g][dt] = and4(vf[g][dt], mk);
@@ -249,6 +253,7 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
   for (int i = 1; i < NW; ++i) M = fmaxf(M, lm[i][r]);
 #pragma unroll
   for (int i = 0; i < NW; ++i) L += ll[i][r] * exp2_fast(lm[i][r] - M);
+  if (lead && pos < 0) L = 0.0f;                 // tiles that the other columns see as a whole are not masked for it
   const float f = exp2_fast(m - M);
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)

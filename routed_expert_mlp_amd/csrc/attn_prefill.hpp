@@ -313,6 +313,22 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
   // values of keys that no column sees, whatever their slots hold, to 0 (all wavefronts)
   auto clear_holes = [&](int v, uint4* slot) __attribute__((always_inline)) {
     const int key0 = key_of(v);
+    if constexpr (LEAD) {
+      // windows of sequences that end inside the prefix may leave gaps between tl.lo and tl.hi
+      if (a.window && p_first < a.shared - 1) {
+        uint64_t any = 0;
+        for (int t = c0 / a.group + lane; t <= (min(c0 + COLS, cols) - 1) / a.group; t += 64) {
+          const int p = attn_position(a, t);
+          any |= visible_bits(key0, min(p, a.shared - 1), attn_window_lo(a, p), tl.sinks);
+        }
+#pragma unroll
+        for (int x = 32; x; x >>= 1) any |= __shfl_xor(any, x);
+        for (int i = tid; i < TS * D / 8; i += NW * 64)
+          slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(any >> (8 * (i / D)))));
+        __syncthreads();
+        return;
+      }
+    }
     if (key0 + TS <= tl.hi && (key0 >= tl.lo || key0 + TS <= tl.sinks)) return;
     for (int i = tid; i < TS * D / 8; i += NW * 64)
       slot[i] = and4(slot[i], value_mask(static_cast<uint32_t>(visible_bits(key0 + 8 * (i / D), tl.hi - 1, tl.lo, tl.sinks))));
@@ -459,7 +475,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
     }
   }
 
-  const float lt = sum_halves(l);
+  float lt = sum_halves(l);
+  if (LEAD && span.pos < 0) lt = 0.0f;           // tiles that the other columns see as a whole are not masked for it
   if (c0 + 32 * w + r >= cols) return;
   const int64_t row = row_of();
   if (!whole) {
