@@ -159,6 +159,8 @@ int moe_attn_decode(const moe_attn_config* cfg, const moe_attn_cache* cache, con
  *             as the table of moe_attn_decode does, or nothing).
  *   seq_lens  [B] int32, the prefix and the new tokens included.  A sequence that
  *             ends inside the prefix (0: a padded row) sees what it has of it.
+ * A value of the prefix that is not finite stays with the new tokens that see it; for
+ * their own keys the new tokens of a sequence are as in moe_attn_decode.
  * Everything else as moe_attn_decode; one prefix a call.  32/8 heads of 128 dims,
  * sequences of up to 256 keys of their own, this call and moe_attn_decode: 4 behind
  * 1024 keys 10.6 and 10.8 us, behind 4096 12.3 and 13.7 us; 16 behind 1024 12.6 and

@@ -50,6 +50,12 @@ struct AttnSeq {
   int n, len, first;
 };
 
+// Column col of a sequence and key/value head: new token col / group, head col % group.
+__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int kvh, int col) {
+  const int t = col / a.group;
+  return (row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
+}
+
 // The same for every lane; said so, because values out of vector loads would
 // otherwise be kept, and worked on, in vector registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -238,5 +244,46 @@ __device__ __forceinline__ uint2 load_stream(const uint2* p) {
 
 // Below every score, and finite: the running maximum of a row that has seen nothing.
 constexpr float ATTN_NO_MAX = -1e30f;
+
+// The columns of a block over the prefix may see different keys of a tile, and a value that one of them sees and that
+// is not finite makes NaN of the weight of 0 that it has for another.  This computes the sums of column col of the
+// batch (position pos, maximum m of the part) over the part's tiles again, by one wavefront, with the keys that the
+// column sees and no others: lane i has the score of key i of 64, then dims i, i + 64 .. of the sums.
+template <int D, int TS>
+__device__ __forceinline__ void attn_part_alone(const AttnArgs& a, const AttnTiles& tl, int kvh, int col, int pos,
+                                                float m, float* sums) {
+  const int lane = threadIdx.x & 63, lo = attn_window_lo(a, pos), last = min(pos, a.shared - 1);
+  const int in_page = (1 << a.page_shift) - 1;
+  const uint16_t* const q = a.q + attn_row(a, 0, kvh, col) * D;
+  auto value = [](uint32_t bf16) { return __uint_as_float(bf16 << 16); };
+  float o[D / 64] = {};
+  for (int i0 = 0; i0 < TS * tl.n; i0 += 64) {
+    const int i = i0 + lane, key = TS * tl.tile(i / TS) + i % TS;
+    const bool sees = i < TS * tl.n && key <= last && (key >= lo || key < tl.sinks);
+    const int at = sees ? key : 0;
+    const int64_t page = min(max(a.shared_pages[at >> a.page_shift], 0), a.n_pages - 1);
+    const int64_t head = ((page * a.kv_heads + kvh) * D) << a.page_shift;
+    const uint16_t* const k = a.k + head + (at & in_page) * 8;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 8) {
+      const bf16x8 kc = *reinterpret_cast<const bf16x8*>(k + (c << a.page_shift));
+      const bf16x8 qc = *reinterpret_cast<const bf16x8*>(q + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(static_cast<float>(kc[j]), static_cast<float>(qc[j]), s);
+    }
+    const float p = sees ? value(f32_to_bf16(exp2_fast(fmaf(s, a.scale_log2, -m)))) : 0.0f;
+    const int64_t from = head + (at & in_page & ~7) * D + (at & 7);
+    for (uint64_t left = __ballot(sees); left; left &= left - 1) {
+      const int l = __builtin_ctzll(left);
+      const float pl = __shfl(p, l);
+      const uint16_t* const v = a.v + __shfl(from, l);
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) o[n] = fmaf(pl, value(v[8 * (lane + 64 * n)]), o[n]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < D / 64; ++n) sums[lane + 64 * n] = o[n];
+}
 
 }  // namespace moe

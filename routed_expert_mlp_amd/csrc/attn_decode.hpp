@@ -46,12 +46,6 @@ constexpr int ATTN_NW = 4;            // wavefronts of a block
 // faster (16 sequences of 4 new tokens, window 4096: 18.4 us, and 19.9 us with 3 or 4).
 constexpr int attn_blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
 
-// Column col of a sequence and key/value head: new token col / group, head col % group.
-__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int64_t row0, int kvh, int col) {
-  const int t = col / a.group;
-  return (row0 + t) * a.heads + kvh * a.group + (col - t * a.group);
-}
-
 // More rows of a head than 32 (heads of the group x new tokens) take several
 // blocks, which read the same keys (AGAIN): through the caches then, around them
 // otherwise (64 sequences of up to 4096 keys, 32/8 heads of 128 dims, one token: 136
@@ -282,6 +276,25 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
         }
     }
   }
+  uint32_t alone = 0;            // columns whose sums attn_part_alone has
+  if (lead && (a.window || first < a.shared - 1)) {        // where columns may see different keys
+    __shared__ uint32_t found;
+    if (w == 0) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += acc[dt][e];
+      const uint64_t nan = __ballot(r < live && L != 0.0f && sum != sum);
+      found = static_cast<uint32_t>(nan | nan >> 32);
+    }
+    __syncthreads();
+    alone = found;
+    for (int i = w; alone && i < live; i += NW)
+      if (alone >> i & 1)
+        attn_part_alone<D, 32>(a, tl, kvh, cb * COLS + i, __shfl(pos, i), __shfl(M, i),
+                               a.pws + ((static_cast<int64_t>(kvh) * cols + cb * COLS + i) * splits + split) * D);
+  }
   if (w != 0 || r >= live) return;
   if (whole) {
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -301,7 +314,8 @@ __global__ __launch_bounds__(ATTN_NW * 64, attn_blocks_per_cu(D)) void k_attn_de
     if constexpr (BEHIND) ml = lead ? a.pml : a.ml;
     else ml = a.ws + static_cast<int64_t>(a.B) * a.kv_heads * cols * splits * D;
     if (half == 0) *reinterpret_cast<float2*>(ml + item * 2) = float2{M, L};
-    if (BEHIND && tl.n == 0) return;             // a part without keys has a sum of 0, and its values are not read
+    // a part without keys has a sum of 0, and its values are not read
+    if (BEHIND && (tl.n == 0 || (alone >> r & 1))) return;
     float* o = sums + item * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)

@@ -477,7 +477,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
 
   float lt = sum_halves(l);
   if (LEAD && span.pos < 0) lt = 0.0f;           // tiles that the other columns see as a whole are not masked for it
-  if (c0 + 32 * w + r >= cols) return;
+  if (!LEAD && c0 + 32 * w + r >= cols) return;
   const int64_t row = row_of();
   if (!whole) {
     int64_t item;
@@ -491,8 +491,30 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_attn_prefill(Attn
       sums = a.ws;
       ml = a.ws + prefill_items(a) * D;
     }
-    if (half == 0) *reinterpret_cast<float2*>(ml + 2 * item) = float2{m, lt};
-    if (LEAD && last < 0) return;                // a part without keys has a sum of 0, and its values are not read
+    if constexpr (LEAD) {
+      const bool mine = c0 + 32 * w + r < cols;
+      uint32_t alone = 0;                        // columns whose sums attn_part_alone has
+      if (a.window || p_first < a.shared - 1) {  // where columns may see different keys
+        float sum = 0.0f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum += acc[dt][e];
+        const uint64_t nan = __ballot(mine && lt != 0.0f && sum != sum);
+        alone = static_cast<uint32_t>(nan | nan >> 32);
+        for (uint32_t left = alone; left; left &= left - 1) {
+          const int i = __builtin_ctz(left);
+          attn_part_alone<D, TS>(a, tl, kvh, c0 + 32 * w + i, __shfl(span.pos, i), __shfl(m, i),
+                                 sums + __shfl(item, i) * D);
+        }
+      }
+      if (!mine) return;
+      if (half == 0) *reinterpret_cast<float2*>(ml + 2 * item) = float2{m, lt};
+      // a part without keys has a sum of 0, and its values are not read
+      if (last < 0 || (alone >> r & 1)) return;
+    } else if (half == 0) {
+      *reinterpret_cast<float2*>(ml + 2 * item) = float2{m, lt};
+    }
     float* o = sums + item * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
