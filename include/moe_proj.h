@@ -102,7 +102,7 @@ int moe_proj_lora_workspace_size(const moe_proj_adapters* adapters, int64_t T, s
  *   out[t] = base[t] + scales[a] * (x[t] A_a^T) B_a^T,   a = adapter[t]
  *   out[t] = base[t]                                      where adapter[t] is not in 0 .. n_adapters - 1
  * with fp32 sums, the inner row x A^T kept to 16 bits of mantissa, and one
- * rounding to bf16.
+ * rounding to bf16; what is not finite is as in fp32.
  *   x       [T, in_features] bf16, rows x_stride apart;
  *   adapter [T] int32;
  *   base    [T, out_features] bf16, rows base_stride apart;

@@ -363,6 +363,28 @@ __global__ __launch_bounds__(64 * LORA_DOWN, GROUPED ? 2 : 4) void k_lora_down(L
   });
 }
 
+// The sums v B of 8 columns of a token again, from v as it is: an infinity in v or in B has none in two halves (the rest
+// of one is inf - inf, and a rest of 0 times one in B is NaN), nor has a v that bf16 rounds up to one.
+__device__ __forceinline__ void lora_whole(const LoraArgs& a, int adapter, int rank, int64_t token, int n, f32x4& s0,
+                                           f32x4& s1) {
+  const uint16_t* const b = a.b + (static_cast<int64_t>(adapter) * a.N + n) * a.R;
+  s0 = s1 = f32x4{};
+#pragma unroll 1
+  for (int r = 0; r < rank; ++r) {
+    const float* at = a.v + token * a.vr + r;
+    float v = 0.0f;
+    for (int p = 0; p < a.parts; ++p, at += a.T * a.vr) v += *at;
+    bool number = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f32x4& s = e < 4 ? s0 : s1;
+      s[e & 3] = fmaf(v, __uint_as_float(static_cast<uint32_t>(b[static_cast<int64_t>(e) * a.R + r]) << 16), s[e & 3]);
+      number |= s[e & 3] == s[e & 3];
+    }
+    if (!number) return;
+  }
+}
+
 // The columns n0 .. n0 + 63 of a tile's tokens from m0 on, MT tiles of 16 of them, by one wavefront of a block that
 // has called it with all of its NW.  v goes to LDS in two bf16 values, upper halves and what is left of them.  The weights of 32
 // ranks at a time, and at the end the sums of 16 tokens, go through LDS of the wavefront's own (`mine`, 4 KB): memory
@@ -469,8 +491,11 @@ __device__ __forceinline__ void lora_columns(const LoraArgs& a, const Tile& tile
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = 8 * h + lr;
-      const f32x4 s0 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp) ^ r));
-      const f32x4 s1 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp + 1) ^ r));
+      f32x4 s0 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp) ^ r));
+      f32x4 s1 = *reinterpret_cast<const f32x4*>(mine + 16 * r + ((2 * lp + 1) ^ r));
+      const f32x4 all = s0 + s1;
+      const float one = (all[0] + all[1]) + (all[2] + all[3]);
+      if (__builtin_expect(one != one, 0)) lora_whole(a, tile.adapter, rank, t[m][h], min(n, a.N - 8), s0, s1);
       lora_piece o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
