@@ -57,8 +57,8 @@ extern "C" {
  * whole, and not each other; no other overlap of an output with another tensor is
  * allowed.  A row with a NaN is NaN in y_out and q_out; one with an infinity is NaN
  * there and 0 elsewhere (x / inf); their scales are finite.  Finite |h| up to 2^56,
- * so that the sum of their squares is finite; with eps 0 that sum has to be 2^-100 at
- * least, or the row one of zeros.
+ * so that the sum of their squares is finite; with eps below 2^-100 that sum has to be
+ * 2^-100 at least, or the row one of zeros.
  */
 int moe_proj_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, const float* weight, float eps,
                   int64_t T, int64_t hidden, uint16_t* h_out, uint16_t* y_out, uint8_t* q_out, float* q_scale,

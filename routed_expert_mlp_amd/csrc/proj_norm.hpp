@@ -166,7 +166,9 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_proj_norm(NormArg
 #pragma unroll
     for (int i = 1; i < WPR; ++i) sum += part[i];
   }
-  const float inv = __builtin_amdgcn_rsqf(fmaf(sum, a.per, a.eps));
+  // the instruction takes numbers below 2^-126 for 0; a factor of 2^96, whose root is exact, keeps them out of its way
+  const float mean = fmaf(sum, a.per, a.eps);
+  const float inv = mean < 0x1p-96f ? __builtin_amdgcn_rsqf(mean * 0x1p96f) * 0x1p48f : __builtin_amdgcn_rsqf(mean);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int p = lane + LANES * i;
