@@ -5,6 +5,7 @@
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -31,16 +32,15 @@ def hipcc():
 
 
 def build(verbose=False):
-    """Compile the sources side by side and link them into LIB; no object stays behind, of which one could be
-    linked into something else after its sources have changed."""
+    """Compile the sources side by side and link them into LIB.  The objects are in a folder of their own, and none of
+    an earlier build stays beside LIB: they could be linked into something else after their sources have changed."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    objs = [os.path.join(LIB_DIR, os.path.basename(src)[:-4] + ".o") for src in SOURCES]
-    try:
-        return _build([hipcc()] + HIPCC_FLAGS, objs, verbose)
-    finally:
-        for obj in objs:
-            if os.path.exists(obj):
-                os.remove(obj)
+    names = [os.path.basename(src)[:-4] + ".o" for src in SOURCES]
+    for old in names:
+        if os.path.exists(os.path.join(LIB_DIR, old)):
+            os.remove(os.path.join(LIB_DIR, old))
+    with tempfile.TemporaryDirectory(prefix="moe_mlp_") as objects:
+        return _build([hipcc()] + HIPCC_FLAGS, [os.path.join(objects, name) for name in names], verbose)
 
 
 def _build(base, objs, verbose):
