@@ -77,6 +77,7 @@ int moe_proj_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
  *   w       [N, K] E4M3;  w_scale [ceil(N / 128), K / 128] fp32;
  *   y       [T, N] bf16.
  *   K a multiple of 128, N of 16, both below MOE_PROJ_MAX_FEATURES;  T * N < 2^32.
+ * A product of two scales that meet has to be a normal fp32 number, or 0.
  */
 int moe_proj_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale, int64_t T, int64_t N,
                  int64_t K, uint16_t* y, void* stream);
@@ -88,7 +89,9 @@ typedef struct moe_proj_adapters {
   const int32_t*  ranks;   /* [n_adapters] int32, clamped to 0 .. max_rank: what a and b hold past it does
                               not matter (NaN too); NULL: max_rank, all of them */
   const float*    scales;  /* [n_adapters] fp32; NULL: ones */
-  int64_t n_adapters;      /* 1 .. 2^20 */
+  int64_t n_adapters;      /* 1 .. 2^20; with 512 or more, however many a call uses, long calls in mixed order read
+                              adapters again for every 64 tokens: 4096 tokens of 50 adapters of rank 32, 4096 columns
+                              to 4096, 55 us with 511 adapters here and 234 us with 512 (in runs 76 us) */
   int32_t max_rank;        /* a multiple of 8 up to MOE_PROJ_LORA_MAX_RANK */
   int32_t in_features;     /* a multiple of 8 below MOE_PROJ_MAX_FEATURES */
   int32_t out_features;    /* a multiple of 8 below MOE_PROJ_MAX_FEATURES */

@@ -38,8 +38,9 @@ bool features_ok(int64_t n, int64_t multiple) { return n >= multiple && n < MOE_
 bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride < kInt32End && stride % 8 == 0; }
 
 // One piece of 8 values a lane as far as 16 wavefronts a row go: the pieces' reductions for the scales follow one
-// another (4096 columns, 4 wavefronts of two or 8 of one: one row 4.0 and 2.8 us, 4096 rows 36.2 and 32.9 us; 8192
-// columns, 4 of four, 8 of two: 4096 rows 70 and 66 us).
+// another.  All outputs, wavefronts of one piece and half as many of two: 4096 columns, one row 2.8 and 3.5 us, 4096
+// rows 30.3 and 31.5 us; 8192 columns, one row 3.7 and 4.1 (and 5.7 of four), 300 rows of 7168 8.1 and 8.6, but 4096
+// rows 61.8 and 58.9.
 template <int WPR, int NV>
 int norm(const NormArgs& a, hipStream_t s) {
   return launch(k_proj_norm<WPR, NV>, dim3(static_cast<unsigned>(WPR == 1 ? cdiv(a.T, 4) : a.T)),
@@ -95,7 +96,11 @@ struct LoraPlan {
 // Every tile of a window reads its adapter again, and the sort is a launch more, of 4 to 10 us: as many tiles are read
 // in less (4096 columns to 4096, windows and sorted: 512 tokens of 3 adapters of rank 16 or 64, 56 tiles, 12.6 and 17.7,
 // 15.9 and 22.1 us; 1024 of them, 112 tiles, 20.9 and 19.9, 27.2 and 27.6; 128 tokens of 32, 72 tiles, 14.2 and 16.0,
-// 20.5 and 20.3; 192 of them, 108 tiles, 19.6 and 15.8, 30.2 and 20.1).
+// 20.5 and 20.3; 192 of them, 108 tiles, 19.6 and 15.8, 30.2 and 20.1).  The rule is that of those sizes: a tile costs
+// by its rank and columns, a sort hardly, so that narrow calls would rather keep their windows (512 columns to 512, rank
+// 8, 2048 tokens of 3 adapters 9.6 and 17.9 us) and wide ones leave them earlier (8192 to 8192, rank 128, 512 tokens of
+// 3 45.0 and 33.9 us).  With LORA_BINS adapters or more, however many of them a call uses, windows are all there is:
+// 4096 tokens of 50 of 511 adapters of rank 32 55 us, of 512 234 us.
 constexpr int64_t LORA_WINDOW_TILES = 80;
 // Blocks of k_lora_down: of a sorted call one a CU, 128 KB of LDS, its unfilled tiles counted too (as many parts as fill
 // 256 with full tiles alone, and this way: 4096 tokens of 50 adapters of rank 32 51 and 46 us, 2000 of 4 of rank 128 43

@@ -178,9 +178,12 @@ __global__ __launch_bounds__(NW * 64) void k_proj_fp8_few(Fp8Args a) {
 //   * There is one barrier a span; the transfers are spread over the products behind
 //     it.
 //   * Transfers past the last row bring zeros (bounds of the buffer).
-// What bounds it: a CU brings about 48 GB/s from outside its L2, whatever the tile
-// (4096 columns: a block of 128 x 128, 1 MB, 22 us, of 256 x 256, 2 MB, 44 us, alone
-// on its CU), so the largest tiles that still fill the GPU are the fastest.  Four slots
+// What bounds it with a block a CU: the chain of a span, its barrier, the reads of its
+// fragments from LDS and their products, which one wavefront a SIMD does in turn: 0.7 us
+// a span (tiles of 128 x 128, 4096 columns, 96 blocks 22.4 us, 192 23.0, 256 23.9; of
+// 256 x 256 44 us).  512 tokens to 6144, the 192 blocks, take 20.8 us without the
+// transfers, 82% of which L2 has, and 16.6 with the first span's fragments throughout.
+// So the largest tiles that still fill the GPU are the fastest.  Four slots
 // where a CU has one block: 512 tokens to 6144 23.4 us, and 25.9 with two; reading the
 // next span's first fragments before its barrier as well: 23.7.
 // 4096 tokens of 4096 columns to 6144: 102-105 us one after the other (117 with pauses,
